@@ -63,7 +63,10 @@ typedef enum {
   THL_E2M3 = 10,  /* OCP fp6 E2M3 (bias 1, all codes finite, max 7.5), bit-packed along the contiguous
                      dimension: element t in bits 6t .. 6t+5 of the little-endian bit stream (four in
                      three bytes) */
-  THL_E3M2 = 11   /* OCP fp6 E3M2 (bias 3, all codes finite, max 28), packed as THL_E2M3 */
+  THL_E3M2 = 11,  /* OCP fp6 E3M2 (bias 3, all codes finite, max 28), packed as THL_E2M3 */
+  THL_I4X2 = 12,  /* two's complement 4-bit integers -8 .. 7, two per byte, even element low nibble
+                     (thl_gemm_w4's weights and thl_moe_gather only) */
+  THL_U4X2 = 13   /* unsigned 4-bit integers 0 .. 15, packed as THL_I4X2 (the same entry points) */
 } thl_dtype;
 
 typedef struct {
@@ -344,6 +347,170 @@ thl_status thl_gemm_grouped(int64_t count, const thl_group_problem* problems,
                             float alpha, float beta, const thl_dtypes* dtypes,
                             const thl_epilogue* epilogue, const thl_scales* scales,
                             struct ihipStream_t* stream);
+
+/*
+ * Operators around a layer's products.  A token's m features are contiguous:
+ * an array of n tokens is a column-major m x n matrix, X(i,j) at X[i + j*ldx],
+ * so that a token-major array is op(B) with opB = N of a product, and its D.
+ * The rules of thl_gemm hold: device pointers owned by the caller, nothing
+ * kept after return, every check before any HIP call, asynchronous on
+ * `stream` (a stream of the current device), reentrant.  These calls allocate
+ * nothing and hold no state of their own: workspaces are the caller's, calls
+ * that may overlap in time need one each, and every call can be captured into
+ * a graph.  Results do not depend on timing.  Arrays are aligned to their
+ * elements (THL_ERR_MISALIGNED otherwise; 8- and 4-bit arrays anywhere); m
+ * above 2^26 and other sizes above INT32_MAX are THL_ERR_UNSUPPORTED.
+ *
+ * thl_rmsnorm -- the root-mean-square norm of each token, the residual added
+ * before it:
+ *   s = x + r,   y_i = q(s_i * w_i / sqrt(mean(s^2) + eps))
+ * in fp32 throughout; S and Y each round once (to nearest even), Y from the
+ * unrounded s.  R = NULL: no residual (s = x; S must be NULL).  S = NULL with
+ * a residual: the sum is not kept.
+ *   types  x: F32, F16 or BF16.  r (R and S): x's type or F32.  w: F32, F16 or
+ *          BF16.  y: F32, F16 or BF16; E4M3 or E5M2 with sfy = NULL: y /
+ *          y_scale, magnitudes past the largest finite value clamped to it
+ *          (y_scale is the product's a_scale or b_scale; 1 for every other
+ *          form); E4M3, E5M2 or E2M1X2 with sfy: MX blocks of 32 consecutive
+ *          features by thl_gemm's MX-output rule, SFY(b, j) at
+ *          sfy[j*ld_sfy + b], ld_sfy >= ceil(m/32) (a product that reads them
+ *          as sfa or sfb wants a multiple of 16), E2M1X2 with ldy even.
+ *   eps    >= 0 and finite.  With eps = 0 a token of zeros is 0/0, NaN.
+ * S may be X or R exactly (same pointer, leading dimension and type), and Y
+ * may be X; any other overlap with an output is THL_ERR_INVALID.
+ */
+typedef struct {
+  thl_dtype x, r, w, y;
+} thl_norm_types;
+
+thl_status thl_rmsnorm(int64_t m, int64_t n, const void* X, int64_t ldx, const void* R, int64_t ldr, void* S,
+                       int64_t lds, const void* W, float eps, float y_scale, void* Y, int64_t ldy, uint8_t* sfy,
+                       int64_t ld_sfy, const thl_norm_types* types, struct ihipStream_t* stream);
+
+/*
+ * thl_rmsnorm_backward -- its gradient (straight through Y's rounding): with
+ * rho = 1/sqrt(mean(s^2) + eps) and h = rho * s,
+ *   dx = rho * (w*dy - h * mean(w*dy*h)) + dr,   dw = sum over tokens of dy*h.
+ * S is what the norm normalised (the forward call's S, or X without a
+ * residual); dx is the gradient of x and of r alike.  DR (may be NULL) is the
+ * gradient that reaches s past the norm.  DW (may be NULL: not wanted) is
+ * written, not added to; with n = 0 it is zeros.
+ *   types      s, w: F32, F16 or BF16.  g (DY, DR and DX): likewise.
+ *              dw: F32 or w's type.
+ *   workspace  thl_rmsnorm_backward_workspace(m, n) bytes, 4-byte aligned, when
+ *              DW is wanted (THL_ERR_INVALID when smaller); not read before it
+ *              is written.
+ * DX may be S, DY or DR exactly; any other overlap with an output or the
+ * workspace is THL_ERR_INVALID.
+ */
+typedef struct {
+  thl_dtype s, w, g, dw;
+} thl_norm_grad_types;
+
+size_t thl_rmsnorm_backward_workspace(int64_t m, int64_t n);
+thl_status thl_rmsnorm_backward(int64_t m, int64_t n, const void* S, int64_t lds, const void* DY, int64_t lddy,
+                                const void* DR, int64_t lddr, const void* W, float eps, void* DX, int64_t lddx,
+                                void* DW, void* workspace, size_t workspace_bytes, const thl_norm_grad_types* types,
+                                struct ihipStream_t* stream);
+
+/*
+ * Tokens sorted by expert and back: the operands and results of a grouped
+ * product whose problems are a layer's experts (problem e: the rows
+ * offsets[e] .. offsets[e+1]-1 of the gathered array).
+ *
+ * thl_moe_sort -- the stable order of n tokens' topk choices by expert.
+ *   ids      ids[j*ld_ids + t], token j's choice t: int32 (ids_bytes = 4) or
+ *            int64 (8).  A value outside 0 .. experts-1 is dropped.  A token
+ *            may choose an expert twice.
+ *   rows     rows[j*topk + t]: the choice's place, -1 when dropped
+ *   offsets  experts+1 values: expert e's first place; offsets[experts] is the
+ *            number of choices kept
+ *   order    (may be NULL) order[place] = j*topk + t; entries past the last
+ *            place are left as they were
+ * Places within an expert follow j*topk + t.  experts <= 1024 and n*topk <=
+ * 2^30 (THL_ERR_UNSUPPORTED above).  workspace: thl_moe_sort_workspace bytes
+ * (0 for up to 4,096 choices), 4-byte aligned; not read before it is written.
+ * No array may overlap another.
+ */
+size_t thl_moe_sort_workspace(int64_t n, int64_t topk, int64_t experts);
+thl_status thl_moe_sort(int64_t n, int64_t topk, int64_t experts, const void* ids, int64_t ld_ids, int ids_bytes,
+                        int32_t* rows, int32_t* offsets, int32_t* order, void* workspace, size_t workspace_bytes,
+                        struct ihipStream_t* stream);
+
+/*
+ * thl_moe_gather -- Y(:, rows[j*topk + t]) = X(:, j) for every choice that has
+ * a place in 0 .. rows_y-1; other columns of Y are left as they were.  Any
+ * format of thl_dtype, copied bit for bit; with sfx and sfy (both or neither)
+ * the ceil(m/32) E8M0 bytes of each token's blocks go along.  For E2M1X2,
+ * I4X2 and U4X2 leading dimensions are even, for E2M3 and E3M2 multiples of
+ * 4; a token's bits past element m in its last byte are copied too.  No
+ * output may overlap another array.  Its gradient is thl_moe_combine without
+ * weights.
+ */
+thl_status thl_moe_gather(int64_t m, int64_t n, int64_t topk, const void* X, int64_t ldx, const uint8_t* sfx,
+                          int64_t ld_sfx, const int32_t* rows, int64_t rows_y, void* Y, int64_t ldy, uint8_t* sfy,
+                          int64_t ld_sfy, thl_dtype type, struct ihipStream_t* stream);
+
+/*
+ * thl_moe_combine -- Y(:, j) = sum over t of weights[j*topk + t] * X(:,
+ * rows[j*topk + t]), in fp32 in the order of t, rounded once.  Choices without
+ * a place in 0 .. rows_x-1 add nothing (and their weight is not read); a token
+ * without any gets zeros.  weights = NULL: ones.  F32, F16 or BF16 for X and
+ * for Y.  Y may not overlap another array.
+ */
+thl_status thl_moe_combine(int64_t m, int64_t n, int64_t topk, const void* X, int64_t ldx, int64_t rows_x,
+                           const int32_t* rows, const float* weights, void* Y, int64_t ldy, thl_dtype type_x,
+                           thl_dtype type_y, struct ihipStream_t* stream);
+
+/*
+ * thl_moe_combine_backward -- its gradient:
+ *   DX(:, rows[j*topk + t]) = weights[j*topk + t] * DY(:, j)
+ *   dweights[j*topk + t] = <DY(:, j), X(:, rows[j*topk + t])>, 0 without a place
+ * DX and dweights may each be NULL (not wanted).  Columns of DX that no choice
+ * has are left as they were.  type_x is X's and DX's.  Places must differ
+ * (thl_moe_sort's do).  DX may be X exactly; no other overlap.
+ */
+thl_status thl_moe_combine_backward(int64_t m, int64_t n, int64_t topk, const void* DY, int64_t lddy, const void* X,
+                                    int64_t ldx, int64_t rows_x, const int32_t* rows, const float* weights, void* DX,
+                                    int64_t lddx, float* dweights, thl_dtype type_dy, thl_dtype type_x,
+                                    struct ihipStream_t* stream);
+
+/*
+ * thl_gemm_w4 -- the product with a matrix of 4-bit weights under group
+ * scales, for a few tokens:
+ *   D(i,j) = act(alpha * sum_g s(i,g) * sum_{p in g} (q(i,p) - z(i,g)) * X(p,j) + beta * C(i,j) + bias[i])
+ * with D and C m x n and X k x n as for thl_gemm (opB = N), and the weights
+ * stored by rows along K: code q(i,p) in nibble p % 2 of byte (i*ldw + p) / 2,
+ * ldw in codes, even, >= k.
+ *   dtypes  a: U4X2 (with zero points), I4X2 or E2M1X2; b (X): F16 or BF16;
+ *           c, d, bias: F32, F16 or BF16; acc: F32.
+ *   scales  s(i,g) for codes g*group .. of row i at scales[i*ld_scales + g]:
+ *           F32, F16 or BF16 for the integer codes, E8M0 for E2M1X2 (an MX fp4
+ *           operand's, group 32).  group: 32, 64, 128 or a larger power of
+ *           two, or any length from k on (one scale a row); the last group of
+ *           a row may be short.  z(i,g) at zeros[i*ld_zeros + g], one byte
+ *           each: required for U4X2, NULL otherwise.
+ * The epilogue is thl_gemm's (sfd unused); D may be C exactly, any other
+ * overlap with D is THL_ERR_INVALID.  Products are exact in fp32; the sum of
+ * a group, its zero point and scale, and the sum over groups round in fp32.
+ * A token that holds an infinity or NaN gives NaN wherever integer codes meet
+ * it; other tokens do not see it.  k = 0 gives act(beta*C + bias).  Any n up
+ * to 2^21, but every 64 tokens stream the weights once more: this call is for
+ * few tokens.
+ */
+typedef struct {
+  const void* scales;
+  int64_t ld_scales;
+  const uint8_t* zeros;
+  int64_t ld_zeros;
+  int64_t group;
+  thl_dtype type; /* of scales */
+} thl_group_scales;
+
+thl_status thl_gemm_w4(int64_t m, int64_t n, int64_t k, const void* W, int64_t ldw, const thl_group_scales* scales,
+                       const void* X, int64_t ldx, const void* C, int64_t ldc, void* D, int64_t ldd, float alpha,
+                       float beta, const thl_dtypes* dtypes, const thl_epilogue* epilogue,
+                       struct ihipStream_t* stream);
 
 /* Static text for a status code. */
 const char* thl_status_string(int status);

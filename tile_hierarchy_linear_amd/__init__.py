@@ -1,8 +1,9 @@
-"""Python binding of libthl.so: the MI355X tiled GEMM with a fused epilogue
-and the Shape:Stride layout module.
+"""Python binding of libthl.so: the MI355X tiled GEMM with a fused epilogue,
+the operators around a layer's products (norm, tokens by expert, 4-bit
+weights), and the Shape:Stride layout module.
 
-Argument marshalling only: every step of the GEMM runs in the library's HIP
-kernels, and the layout algebra in its C++.  The names match the C entry
+Argument marshalling only: every step of the GEMM and of the operators runs
+in the library's HIP kernels, and the layout algebra in its C++.  The names match the C entry
 points of ``include/thl.h``.  Importing this module fails loudly when the
 built library is missing; there is no fallback.
 """
@@ -19,7 +20,7 @@ THL_OK, THL_ERR_INVALID, THL_ERR_UNSUPPORTED, THL_ERR_MISALIGNED, THL_ERR_HIP, T
 THL_ERR_SCRATCH = -6
 THL_OP_N, THL_OP_T = 0, 1
 DTYPES = {"f32": 0, "f16": 1, "bf16": 2, "i8": 3, "i32": 4, "e4m3": 5, "e2m1": 6, "e8m0": 7, "none": 8, "e5m2": 9,
-          "e2m3": 10, "e3m2": 11}
+          "e2m3": 10, "e3m2": 11, "i4": 12, "u4": 13}
 THL_EPI_NONE, THL_EPI_BIAS, THL_EPI_RELU, THL_EPI_GELU = 0, 1, 2, 4
 
 
@@ -50,6 +51,19 @@ class thl_group_problem(ctypes.Structure):
                 ("C", ctypes.c_void_p), ("ldc", ctypes.c_int64), ("D", ctypes.c_void_p), ("ldd", ctypes.c_int64),
                 ("bias", ctypes.c_void_p), ("sfa", ctypes.c_void_p), ("ld_sfa", ctypes.c_int64),
                 ("sfb", ctypes.c_void_p), ("ld_sfb", ctypes.c_int64)]
+
+
+class thl_norm_types(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_int), ("r", ctypes.c_int), ("w", ctypes.c_int), ("y", ctypes.c_int)]
+
+
+class thl_norm_grad_types(ctypes.Structure):
+    _fields_ = [("s", ctypes.c_int), ("w", ctypes.c_int), ("g", ctypes.c_int), ("dw", ctypes.c_int)]
+
+
+class thl_group_scales(ctypes.Structure):
+    _fields_ = [("scales", ctypes.c_void_p), ("ld_scales", ctypes.c_int64), ("zeros", ctypes.c_void_p),
+                ("ld_zeros", ctypes.c_int64), ("group", ctypes.c_int64), ("type", ctypes.c_int)]
 
 
 def _load():
@@ -83,6 +97,24 @@ def _load():
                                      ctypes.c_float, ctypes.c_float, ctypes.POINTER(thl_dtypes),
                                      ctypes.POINTER(thl_epilogue), ctypes.POINTER(thl_scales), vp]
     lib.thl_gemm_grouped.restype = ctypes.c_int
+    f32, i32 = ctypes.c_float, ctypes.c_int
+    lib.thl_rmsnorm.argtypes = [i64, i64, vp, i64, vp, i64, vp, i64, vp, f32, f32, vp, i64, vp, i64,
+                                ctypes.POINTER(thl_norm_types), vp]
+    lib.thl_rmsnorm_backward_workspace.argtypes = [i64, i64]
+    lib.thl_rmsnorm_backward.argtypes = [i64, i64, vp, i64, vp, i64, vp, i64, vp, f32, vp, i64, vp, vp, sz,
+                                         ctypes.POINTER(thl_norm_grad_types), vp]
+    lib.thl_moe_sort_workspace.argtypes = [i64, i64, i64]
+    lib.thl_moe_sort.argtypes = [i64, i64, i64, vp, i64, i32, vp, vp, vp, vp, sz, vp]
+    lib.thl_moe_gather.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp]
+    lib.thl_moe_combine.argtypes = [i64, i64, i64, vp, i64, i64, vp, vp, vp, i64, i32, i32, vp]
+    lib.thl_moe_combine_backward.argtypes = [i64, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp, i64, vp, i32, i32, vp]
+    lib.thl_gemm_w4.argtypes = [i64, i64, i64, vp, i64, ctypes.POINTER(thl_group_scales), vp, i64, vp, i64, vp, i64,
+                                f32, f32, ctypes.POINTER(thl_dtypes), ctypes.POINTER(thl_epilogue), vp]
+    for name in ("rmsnorm", "rmsnorm_backward", "moe_sort", "moe_gather", "moe_combine", "moe_combine_backward",
+                 "gemm_w4"):
+        getattr(lib, "thl_" + name).restype = ctypes.c_int
+    for name in ("rmsnorm_backward_workspace", "moe_sort_workspace"):
+        getattr(lib, "thl_" + name).restype = sz
     lib.thl_status_string.argtypes = [ctypes.c_int]
     lib.thl_status_string.restype = cp
     lib.thl_last_variant.restype = cp
@@ -277,6 +309,336 @@ def thl_kernel_index_map(name: str, points, params=()) -> list[tuple[int, int]]:
 
 def thl_kernel_index_map_names() -> list[str]:
     return _lib.thl_kernel_index_map_names().decode().split(",")
+
+
+# ------------------------------------------------------------------ operators around the products
+# Direct calls of the C entry points, arguments as in include/thl.h (pointers
+# are integers or None, the types structures objects, formats names or codes).
+
+def _ref(structure):
+    return ctypes.byref(structure) if structure is not None else None
+
+
+def thl_rmsnorm(m, n, X, ldx, R, ldr, S, lds, W, eps, y_scale, Y, ldy, sfy, ld_sfy, types, stream=None) -> int:
+    return _lib.thl_rmsnorm(m, n, X, ldx, R, ldr, S, lds, W, eps, y_scale, Y, ldy, sfy, ld_sfy, _ref(types), stream)
+
+
+def thl_rmsnorm_backward_workspace(m, n) -> int:
+    return _lib.thl_rmsnorm_backward_workspace(m, n)
+
+
+def thl_rmsnorm_backward(m, n, S, lds, DY, lddy, DR, lddr, W, eps, DX, lddx, DW, workspace, workspace_bytes, types,
+                         stream=None) -> int:
+    return _lib.thl_rmsnorm_backward(m, n, S, lds, DY, lddy, DR, lddr, W, eps, DX, lddx, DW, workspace,
+                                     workspace_bytes, _ref(types), stream)
+
+
+def thl_moe_sort_workspace(n, topk, experts) -> int:
+    return _lib.thl_moe_sort_workspace(n, topk, experts)
+
+
+def thl_moe_sort(n, topk, experts, ids, ld_ids, ids_bytes, rows, offsets, order, workspace, workspace_bytes,
+                 stream=None) -> int:
+    return _lib.thl_moe_sort(n, topk, experts, ids, ld_ids, ids_bytes, rows, offsets, order, workspace,
+                             workspace_bytes, stream)
+
+
+def thl_moe_gather(m, n, topk, X, ldx, sfx, ld_sfx, rows, rows_y, Y, ldy, sfy, ld_sfy, type, stream=None) -> int:
+    return _lib.thl_moe_gather(m, n, topk, X, ldx, sfx, ld_sfx, rows, rows_y, Y, ldy, sfy, ld_sfy, _dt(type), stream)
+
+
+def thl_moe_combine(m, n, topk, X, ldx, rows_x, rows, weights, Y, ldy, type_x, type_y, stream=None) -> int:
+    return _lib.thl_moe_combine(m, n, topk, X, ldx, rows_x, rows, weights, Y, ldy, _dt(type_x), _dt(type_y), stream)
+
+
+def thl_moe_combine_backward(m, n, topk, DY, lddy, X, ldx, rows_x, rows, weights, DX, lddx, dweights, type_dy, type_x,
+                             stream=None) -> int:
+    return _lib.thl_moe_combine_backward(m, n, topk, DY, lddy, X, ldx, rows_x, rows, weights, DX, lddx, dweights,
+                                         _dt(type_dy), _dt(type_x), stream)
+
+
+def thl_gemm_w4(m, n, k, W, ldw, scales, X, ldx, C, ldc, D, ldd, alpha, beta, dtypes, epilogue=None,
+                stream=None) -> int:
+    return _lib.thl_gemm_w4(m, n, k, W, ldw, _ref(scales), X, ldx, C, ldc, D, ldd, alpha, beta, _ref(dtypes),
+                            _ref(epilogue), stream)
+
+
+# Torch-tensor forms.  An array of tokens is a (tokens, features) tensor whose
+# features are contiguous (rows may be pitched); outputs are tensors that the
+# caller made, so that serving loops and graphs reuse them.  They issue on the
+# current stream of the tensors' device, take their workspaces from torch on
+# that stream, and raise ValueError for a tensor of the wrong shape, type or
+# device and ThlError for what the library refuses.
+
+def _torch_formats():
+    import torch
+
+    codes = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16", torch.int8: "i8",
+             torch.uint8: "i8", torch.int32: "i32", torch.float8_e4m3fn: "e4m3", torch.float8_e5m2: "e5m2",
+             torch.float8_e8m0fnu: "e8m0"}
+    return {t: DTYPES[c] for t, c in codes.items()}
+
+
+_FORMATS: dict = {}
+
+
+def _format(t) -> int:
+    if not _FORMATS:
+        _FORMATS.update(_torch_formats())
+    f = _FORMATS.get(t.dtype)
+    if f is None:
+        raise ValueError(f"no format for tensors of {t.dtype}")
+    return f
+
+
+def _tokens(what, t, like=None, n=None, m=None):
+    """A (tokens, features) tensor's address and leading dimension."""
+    if t.dim() != 2 or not t.is_cuda or (like is not None and t.device != like.device):
+        raise ValueError(f"{what}: a (tokens, features) tensor on the same GPU as the others")
+    rows, cols = t.shape
+    if (n is not None and rows != n) or (m is not None and cols != m):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected ({n}, {m})")
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{what}: features must be contiguous")
+    return t.data_ptr(), ld if rows > 1 else max(ld, cols, 1)
+
+
+def _flat(what, t, like, shape, dtypes):
+    """A contiguous tensor's address."""
+    if tuple(t.shape) != shape or t.dtype not in dtypes or t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous tensor of shape {shape} and type {dtypes} on the others' GPU")
+    return t.data_ptr()
+
+
+def _scale_bytes(what, t, like, n, blocks):
+    """An E8M0 scale array's address and leading dimension (tokens x at least `blocks`)."""
+    if t.element_size() != 1:
+        raise ValueError(f"{what}: one byte a scale")
+    p, ld = _tokens(what, t, like, n)
+    if t.shape[1] < blocks:
+        raise ValueError(f"{what}: {t.shape[1]} scales a token, expected {blocks}")
+    return p, ld
+
+
+class _On:
+    """Makes the tensors' device current around a launch, and names its current stream."""
+
+    __slots__ = ("device", "before")
+
+    def __init__(self, like):
+        self.device = like.device.index
+
+    def __enter__(self):
+        import torch
+
+        self.before = torch.cuda.current_device()
+        if self.before != self.device:
+            torch.cuda.set_device(self.device)
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *_):
+        if self.before != self.device:
+            import torch
+
+            torch.cuda.set_device(self.before)
+
+
+def _check(status, what):
+    if status != THL_OK:
+        raise ThlError(status, what)
+
+
+def rmsnorm(x, w, y, *, eps=1e-6, residual=None, residual_out=None, scale=1.0, sf=None):
+    """y = the root-mean-square norm of x (+ residual) times w, in y's format; the sum goes to residual_out.
+    An fp8 y holds y / scale, or MX blocks when sf takes their E8M0 scales; a uint8 y of ceil(features / 2)
+    columns holds E2M1 MX blocks.  Returns y."""
+    import torch
+
+    n, m = x.shape
+    px, ldx = _tokens("x", x)
+    fp4 = y.dtype == torch.uint8
+    py, ldy = _tokens("y", y, x, n, (m + 1) // 2 if fp4 else m)
+    types = thl_norm_types(_format(x), DTYPES["none"], _format(w), DTYPES["e2m1"] if fp4 else _format(y))
+    pw = _flat("w", w, x, (m,), (w.dtype,))
+    pr = ldr = ps = lds = pf = ldf = 0
+    if residual is not None:
+        pr, ldr = _tokens("residual", residual, x, n, m)
+        types.r = _format(residual)
+    if residual_out is not None:
+        if residual is None or residual_out.dtype != residual.dtype:
+            raise ValueError("residual_out: with a residual, of its type")
+        ps, lds = _tokens("residual_out", residual_out, x, n, m)
+    if sf is not None:
+        pf, ldf = _scale_bytes("sf", sf, x, n, (m + 31) // 32)
+    with _On(x) as stream:
+        _check(_lib.thl_rmsnorm(m, n, px, ldx, pr, ldr, ps, lds, pw, eps, scale, py, 2 * ldy if fp4 else ldy, pf, ldf,
+                                ctypes.byref(types), stream), "thl_rmsnorm")
+    return y
+
+
+def rmsnorm_backward(s, dy, w, dx, dw=None, *, eps=1e-6, dres=None):
+    """The gradients of rmsnorm for the s it normalised: dx (of x and residual alike; dres, the gradient that
+    reaches s past the norm, is added) and, if wanted, dw."""
+    import torch
+
+    n, m = s.shape
+    ps, lds = _tokens("s", s)
+    pg, ldg = _tokens("dy", dy, s, n, m)
+    px, ldx = _tokens("dx", dx, s, n, m)
+    pw = _flat("w", w, s, (m,), (w.dtype,))
+    pr = ldr = 0
+    if dres is not None:
+        pr, ldr = _tokens("dres", dres, s, n, m)
+    if dx.dtype != dy.dtype or (dres is not None and dres.dtype != dy.dtype):
+        raise ValueError("dy, dres and dx have one type")
+    types = thl_norm_grad_types(_format(s), _format(w), _format(dy), DTYPES["none"])
+    pd = size = pws = 0
+    if dw is not None:
+        pd = _flat("dw", dw, s, (m,), (dw.dtype,))
+        types.dw = _format(dw)
+    with _On(s) as stream:
+        if pd:
+            size = _lib.thl_rmsnorm_backward_workspace(m, n)
+            workspace = torch.empty(size, dtype=torch.uint8, device=s.device)
+            pws = workspace.data_ptr()
+        _check(_lib.thl_rmsnorm_backward(m, n, ps, lds, pg, ldg, pr, ldr, pw, eps, px, ldx, pd, pws, size,
+                                         ctypes.byref(types), stream), "thl_rmsnorm_backward")
+
+
+def moe_sort(ids, experts, rows, offsets, *, order=None):
+    """The stable order of (tokens, choices) int32 or int64 expert ids: each choice's row (int32, -1 when its id is
+    outside 0 .. experts-1), each expert's first row (experts + 1 of them), and each row's flat choice."""
+    import torch
+
+    n, topk = ids.shape
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("ids: int32 or int64")
+    pi, ld = _tokens("ids", ids)
+    i32 = (torch.int32,)
+    pr = _flat("rows", rows, ids, (n, topk), i32)
+    pf = _flat("offsets", offsets, ids, (experts + 1,), i32)
+    po = _flat("order", order, ids, (n * topk,), i32) if order is not None else 0
+    with _On(ids) as stream:
+        size, pws = _lib.thl_moe_sort_workspace(n, topk, experts), 0
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=ids.device)
+            pws = workspace.data_ptr()
+        _check(_lib.thl_moe_sort(n, topk, experts, pi, ld, ids.element_size(), pr, pf, po, pws, size, stream),
+               "thl_moe_sort")
+
+
+def _choices(rows, like):
+    import torch
+
+    if rows.dim() != 2:
+        raise ValueError("rows: (tokens, choices)")
+    return _flat("rows", rows, like, tuple(rows.shape), (torch.int32,)), rows.shape[0], rows.shape[1]
+
+
+def moe_gather(x, rows, y, *, sf=None, sf_y=None, type_x=None):
+    """y[rows[j, t]] = x[j], bit for bit, with the rows of block scales sf likewise into sf_y.  type_x: "e2m1" (two
+    codes a byte of a uint8 tensor) where the tensor's type does not say it."""
+    pr, n, topk = _choices(rows, x)
+    px, ldx = _tokens("x", x, None, n)
+    if y.dtype != x.dtype:
+        raise ValueError("y has x's type")
+    py, ldy = _tokens("y", y, x, None, x.shape[1])
+    packed = 1
+    if type_x is not None:
+        if x.element_size() != 1 or type_x not in ("e2m1", "e4m3", "e5m2", "i8", "i4", "u4"):
+            raise ValueError("type_x: an 8- or 4-bit format of a one-byte tensor")
+        packed = 2 if type_x in ("e2m1", "i4", "u4") else 1
+    m = packed * x.shape[1]
+    pf = ldf = pg = ldg = 0
+    if (sf is None) != (sf_y is None):
+        raise ValueError("sf and sf_y go together")
+    if sf is not None:
+        pf, ldf = _scale_bytes("sf", sf, x, n, (m + 31) // 32)
+        pg, ldg = _scale_bytes("sf_y", sf_y, x, y.shape[0], (m + 31) // 32)
+    with _On(x) as stream:
+        _check(_lib.thl_moe_gather(m, n, topk, px, packed * ldx, pf, ldf, pr, y.shape[0], py, packed * ldy, pg, ldg,
+                                   DTYPES[type_x] if type_x else _format(x), stream), "thl_moe_gather")
+    return y
+
+
+def moe_combine(x, rows, y, *, weights=None):
+    """y[j] = the sum over t of weights[j, t] * x[rows[j, t]] (fp32 weights, ones without).  Returns y."""
+    import torch
+
+    pr, n, topk = _choices(rows, x)
+    px, ldx = _tokens("x", x)
+    py, ldy = _tokens("y", y, x, n, x.shape[1])
+    pw = _flat("weights", weights, x, (n, topk), (torch.float32,)) if weights is not None else 0
+    with _On(x) as stream:
+        _check(_lib.thl_moe_combine(x.shape[1], n, topk, px, ldx, x.shape[0], pr, pw, py, ldy, _format(x), _format(y),
+                                    stream), "thl_moe_combine")
+    return y
+
+
+def moe_combine_backward(dy, x, rows, weights, dx=None, dweights=None):
+    """moe_combine's gradients: dx (x's type; rows that no choice has are left as they were) and dweights (fp32),
+    each if wanted.  Without dweights x may be None (dx gives the rows)."""
+    import torch
+
+    like = x if x is not None else dx
+    if like is None or (dweights is not None and x is None):
+        raise ValueError("x is needed for dweights, x or dx for the rows")
+    pr, n, topk = _choices(rows, dy)
+    m = like.shape[1]
+    pg, ldg = _tokens("dy", dy, None, n, m)
+    px = ldx = pd = ldd = pw = pv = 0
+    if x is not None:
+        px, ldx = _tokens("x", x, dy)
+    if dx is not None:
+        pd, ldd = _tokens("dx", dx, dy, like.shape[0], m)
+        if dx.dtype != like.dtype:
+            raise ValueError("dx has x's type")
+        pw = _flat("weights", weights, dy, (n, topk), (torch.float32,))
+    if dweights is not None:
+        pv = _flat("dweights", dweights, dy, (n, topk), (torch.float32,))
+    with _On(dy) as stream:
+        _check(_lib.thl_moe_combine_backward(m, n, topk, pg, ldg, px, ldx, like.shape[0], pr, pw, pd, ldd, pv,
+                                             _format(dy), _format(like), stream), "thl_moe_combine_backward")
+
+
+def gemm_w4(w, x, d, *, scales, group, type_w="u4", zeros=None, c=None, alpha=1.0, beta=0.0, bias=None, act="none"):
+    """d = act(alpha * x @ W^T + beta * c + bias) for (features, K / 2) uint8 weights of two codes a byte ("u4" with
+    uint8 zero points, "i4", or "e2m1" with E8M0 scales), (features, groups) scales and (tokens, K) x.  Returns d."""
+    n, k = x.shape
+    m = w.shape[0]
+    if w.element_size() != 1 or type_w not in ("u4", "i4", "e2m1"):
+        raise ValueError("w: two codes a byte, u4, i4 or e2m1")
+    if group < 1:
+        raise ValueError("group: a positive length")
+    pw, ldw = _tokens("w", w, x, m, (k + 1) // 2)
+    px, ldx = _tokens("x", x)
+    pd, ldd = _tokens("d", d, x, n, m)
+    groups = -(-k // group)
+    dts = thl_dtypes(DTYPES[type_w], _format(x), DTYPES["f32"], _format(d), DTYPES["none"], DTYPES["f32"])
+    if type_w == "e2m1":
+        ps, lds = _scale_bytes("scales", scales, x, m, groups)
+        ts = DTYPES["e8m0"]
+    else:
+        ps, lds = _tokens("scales", scales, x, m, groups)
+        ts = _format(scales)
+    pz, ldz = _scale_bytes("zeros", zeros, x, m, groups) if zeros is not None else (0, 0)
+    gs = thl_group_scales(ps, lds, pz, ldz, group, ts)
+    pc = ldc = 0
+    if beta != 0.0:
+        if c is None:
+            raise ValueError("beta without c")
+        pc, ldc = _tokens("c", c, x, n, m)
+        dts.c = _format(c)
+    epi = thl_epilogue({"none": 0, "relu": THL_EPI_RELU, "gelu": THL_EPI_GELU}[act], None, None, 0)
+    if bias is not None:
+        epi.flags |= THL_EPI_BIAS
+        epi.bias = _flat("bias", bias, x, (m,), (bias.dtype,))
+        dts.bias = _format(bias)
+    with _On(x) as stream:
+        _check(_lib.thl_gemm_w4(m, n, k, pw, 2 * ldw, ctypes.byref(gs), px, ldx, pc, ldc, pd, ldd, alpha, beta,
+                                ctypes.byref(dts), ctypes.byref(epi), stream), "thl_gemm_w4")
+    return d
 
 
 # ------------------------------------------------------------------ layouts

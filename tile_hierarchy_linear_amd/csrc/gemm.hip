@@ -27,6 +27,7 @@
 #include "../../include/thl.h"
 #include "convert.hpp"
 #include "gemm_args.hpp"
+#include "host_checks.hpp"
 #include "index_maps.hpp"
 
 namespace thl {
@@ -281,57 +282,16 @@ int family_of(thl_dtype t) {
   }
 }
 
-// Bytes of `count` elements of a format (fp4: two per byte, rounded up).
-int64_t bytes_of(thl_dtype t, int64_t count) {
-  switch (t) {
-    case THL_F32:
-    case THL_I32:
-      return 4 * count;
-    case THL_F16:
-    case THL_BF16:
-      return 2 * count;
-    case THL_I8:
-    case THL_E4M3:
-    case THL_E5M2:
-    case THL_E8M0:
-      return count;
-    case THL_E2M1X2:
-      return (count + 1) / 2;
-    case THL_E2M3:
-    case THL_E3M2:
-      return (6 * count + 7) / 8;
-    default:
-      return 0;
-  }
-}
-
 // Bits of one element of an operand format.
 int bits_of(thl_dtype t) {
   return t == THL_E2M1X2 ? 4 : ((t == THL_E2M3 || t == THL_E3M2) ? 6 : 8 * static_cast<int>(bytes_of(t, 1)));
 }
-
-bool is_float_io(thl_dtype t) { return t == THL_F32 || t == THL_F16 || t == THL_BF16; }
 
 // D formats written as MX blocks (elements plus generated E8M0 scales).
 int mx_out_of(thl_dtype t) {
   return t == THL_E4M3 ? MX_E4M3 : (t == THL_E5M2 ? MX_E5M2 : (t == THL_E2M1X2 ? MX_E2M1 : MX_NONE));
 }
 bool is_mx_out(thl_dtype t) { return mx_out_of(t) != MX_NONE; }
-
-struct Range {
-  uintptr_t lo = 0, hi = 0;  // [lo, hi), empty when lo == hi
-};
-
-// Byte range spanned by a column-major r x c matrix with leading dimension ld.
-Range matrix_range(const void* p, thl_dtype t, int64_t r, int64_t c, int64_t ld) {
-  Range g;
-  if (!p || r <= 0 || c <= 0) return g;
-  g.lo = reinterpret_cast<uintptr_t>(p);
-  g.hi = g.lo + static_cast<uintptr_t>(bytes_of(t, (c - 1) * ld + r));
-  return g;
-}
-
-bool overlaps(const Range& a, const Range& b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
 
 // Batched problems (L mode): `count` problems whose arrays lie at fixed
 // strides, in elements of each array's own format (E8M0 bytes for scales).
