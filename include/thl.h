@@ -485,7 +485,7 @@ thl_status thl_moe_combine_backward(int64_t m, int64_t n, int64_t topk, const vo
  *   dtypes  a: U4X2 (with zero points), I4X2 or E2M1X2; b (X): F16 or BF16;
  *           c, d, bias: F32, F16 or BF16; acc: F32.
  *   scales  s(i,g) for codes g*group .. of row i at scales[i*ld_scales + g]:
- *           F32, F16 or BF16 for the integer codes, E8M0 for E2M1X2 (an MX fp4
+ *           F16 or BF16 for the integer codes, E8M0 for E2M1X2 (an MX fp4
  *           operand's, group 32).  group: 32, 64, 128 or a larger power of
  *           two, or any length from k on (one scale a row); the last group of
  *           a row may be short.  z(i,g) at zeros[i*ld_zeros + g], one byte
@@ -495,8 +495,11 @@ thl_status thl_moe_combine_backward(int64_t m, int64_t n, int64_t topk, const vo
  * a group, its zero point and scale, and the sum over groups round in fp32.
  * A token that holds an infinity or NaN gives NaN wherever integer codes meet
  * it; other tokens do not see it.  k = 0 gives act(beta*C + bias).  Any n up
- * to 2^21, but every 64 tokens stream the weights once more: this call is for
+ * to 2^19, but every 64 tokens stream the weights once more: this call is for
  * few tokens.
+ *   workspace  thl_gemm_w4_workspace(n, k) bytes (0 for up to 4 tokens),
+ *              16-byte aligned; not read before it is written, overlapping
+ *              nothing (THL_ERR_INVALID when smaller).
  */
 typedef struct {
   const void* scales;
@@ -507,10 +510,11 @@ typedef struct {
   thl_dtype type; /* of scales */
 } thl_group_scales;
 
+size_t thl_gemm_w4_workspace(int64_t n, int64_t k);
 thl_status thl_gemm_w4(int64_t m, int64_t n, int64_t k, const void* W, int64_t ldw, const thl_group_scales* scales,
                        const void* X, int64_t ldx, const void* C, int64_t ldc, void* D, int64_t ldd, float alpha,
-                       float beta, const thl_dtypes* dtypes, const thl_epilogue* epilogue,
-                       struct ihipStream_t* stream);
+                       float beta, const thl_dtypes* dtypes, const thl_epilogue* epilogue, void* workspace,
+                       size_t workspace_bytes, struct ihipStream_t* stream);
 
 /* Static text for a status code. */
 const char* thl_status_string(int status);

@@ -82,6 +82,9 @@ def test_workspace_sizes():
     assert thl.thl_moe_sort_workspace(512, 8, 64) == 0
     assert thl.thl_moe_sort_workspace(513, 8, 64) > 0
     assert thl.thl_moe_sort_workspace(1 << 26, 8, 64) <= 256 * 64 * 4
+    assert thl.thl_gemm_w4_workspace(4, 4096) == thl.thl_gemm_w4_workspace(40, 0) == 0
+    assert thl.thl_gemm_w4_workspace(5, 4096) == 16 * 4096 * 2
+    assert thl.thl_gemm_w4_workspace(17, 256) == 32 * 512 and thl.thl_gemm_w4_workspace(65, 257) == 128 * 1024
     assert thl.thl_moe_sort_workspace(-1, 8, 64) == thl.thl_moe_sort_workspace(513, 8, 1 << 20) == 0
 
 
@@ -155,12 +158,12 @@ def test_moe_combine_backward_refusals(kw, want):
 
 def w4(m=64, n=4, k=256, w=P[0], ldw=256, scales=P[1], ld_s=2, zeros=P[2], ld_z=2, group=128, ts="f16", x=P[3],
        ldx=256, c=None, ldc=64, d=P[4], ldd=64, beta=0.0, types=("u4", "f16", "f16", "f16", "none"), flags=0,
-       bias=None, acc="f32", gs=True):
+       bias=None, acc="f32", gs=True, ws=None, size=0):
     ta, tb, tc, td, tbias = types
     dts = thl.make_dtypes(ta, tb, tc, td, tbias, acc)
     sc = thl.thl_group_scales(scales, ld_s, zeros, ld_z, group, D[ts]) if gs else None
     return thl.thl_gemm_w4(m, n, k, w, ldw, sc, x, ldx, c, ldc, d, ldd, 1.0, beta, dts,
-                           thl.thl_epilogue(flags, bias, None, 0))
+                           thl.thl_epilogue(flags, bias, None, 0), ws, size)
 
 
 I4 = ("i4", "bf16", "f32", "f32", "none")
@@ -177,11 +180,15 @@ E2 = ("e2m1", "bf16", "f32", "f32", "none")
     (dict(group=0), INVALID), (dict(group=16), UNSUPPORTED), (dict(group=96), UNSUPPORTED),
     (dict(types=I4), UNSUPPORTED),  # signed codes with zero points
     (dict(types=I4, zeros=None, ts="e8m0"), UNSUPPORTED), (dict(types=E2, zeros=None), UNSUPPORTED),
+    (dict(ts="f32"), UNSUPPORTED),
     (dict(types=E2, zeros=None, ts="e8m0", group=64), UNSUPPORTED),
     (dict(types=("e4m3", "f16", "f16", "f16", "none")), UNSUPPORTED),
     (dict(types=("u4", "f32", "f16", "f16", "none")), UNSUPPORTED),
     (dict(types=("u4", "f16", "f16", "e4m3", "none")), UNSUPPORTED), (dict(acc="i32"), UNSUPPORTED),
-    (dict(m=1 << 27), UNSUPPORTED), (dict(n=1 << 22), UNSUPPORTED),
+    (dict(m=1 << 27), UNSUPPORTED), (dict(n=1 << 20), UNSUPPORTED),
+    (dict(n=17), INVALID), (dict(n=17, ws=P[6], size=32 * 512 - 1), INVALID),
+    (dict(n=17, ws=P[6] + 8, size=1 << 20), MISALIGNED), (dict(n=17, ws=P[4], size=1 << 20), INVALID),
+    (dict(n=17, ws=P[0], size=1 << 20), INVALID), (dict(n=17, ws=P[3], size=1 << 20), INVALID),
     (dict(x=P[3] + 1), MISALIGNED), (dict(d=P[4] + 1), MISALIGNED), (dict(scales=P[1] + 1), MISALIGNED),
     (dict(d=P[0]), INVALID), (dict(d=P[1]), INVALID), (dict(d=P[2]), INVALID), (dict(d=P[3]), INVALID),
     (dict(beta=1.0, c=P[4], ldc=80), INVALID), (dict(m=0), OK), (dict(n=0), OK),

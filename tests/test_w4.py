@@ -78,7 +78,7 @@ def test_features(m):
         _run(m, n, 768, "u4", 128, seed=m)
 
 
-@pytest.mark.parametrize("ts", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("ts", ["f16", "bf16"])
 def test_scale_types_and_pitched_rows_at_byte_offsets(ts):
     for offset in (0, 1, 5):
         for k in (512, 700):
@@ -117,7 +117,7 @@ def test_every_code_and_zero_point():
     m, k = 64, 512
     q = torch.arange(m) % 16
     w = (q | (q << 4)).to(torch.uint8)[:, None].expand(m, k // 2).contiguous().cuda()
-    scales = torch.full((m, 16), 0.5, device="cuda")
+    scales = torch.full((m, 16), 0.5, dtype=torch.float16, device="cuda")
     zeros = (torch.arange(16)[None, :] + torch.arange(m)[:, None]).remainder(16).to(torch.uint8).cuda()
     for x in ("bf16", "f16"):
         xt = torch.zeros(16, k, dtype=F[x], device="cuda")
@@ -170,7 +170,7 @@ def test_k_zero_is_the_epilogue():
     bias = torch.randn(20, device="cuda")
     d = torch.empty(3, 20, device="cuda")
     e = torch.empty(3, 0, dtype=torch.bfloat16, device="cuda")
-    thl.gemm_w4(torch.empty(20, 0, dtype=torch.uint8, device="cuda"), e, d, scales=torch.empty(20, 0, device="cuda"),
+    thl.gemm_w4(torch.empty(20, 0, dtype=torch.uint8, device="cuda"), e, d, scales=torch.empty(20, 0, dtype=torch.float16, device="cuda"),
                 group=32, type_w="i4", bias=bias, act="relu")
     torch.cuda.synchronize()
     assert torch.equal(d, bias.clamp(min=0).expand(3, 20))

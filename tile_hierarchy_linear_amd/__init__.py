@@ -109,11 +109,12 @@ def _load():
     lib.thl_moe_combine.argtypes = [i64, i64, i64, vp, i64, i64, vp, vp, vp, i64, i32, i32, vp]
     lib.thl_moe_combine_backward.argtypes = [i64, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp, i64, vp, i32, i32, vp]
     lib.thl_gemm_w4.argtypes = [i64, i64, i64, vp, i64, ctypes.POINTER(thl_group_scales), vp, i64, vp, i64, vp, i64,
-                                f32, f32, ctypes.POINTER(thl_dtypes), ctypes.POINTER(thl_epilogue), vp]
+                                f32, f32, ctypes.POINTER(thl_dtypes), ctypes.POINTER(thl_epilogue), vp, sz, vp]
+    lib.thl_gemm_w4_workspace.argtypes = [i64, i64]
     for name in ("rmsnorm", "rmsnorm_backward", "moe_sort", "moe_gather", "moe_combine", "moe_combine_backward",
                  "gemm_w4"):
         getattr(lib, "thl_" + name).restype = ctypes.c_int
-    for name in ("rmsnorm_backward_workspace", "moe_sort_workspace"):
+    for name in ("rmsnorm_backward_workspace", "moe_sort_workspace", "gemm_w4_workspace"):
         getattr(lib, "thl_" + name).restype = sz
     lib.thl_status_string.argtypes = [ctypes.c_int]
     lib.thl_status_string.restype = cp
@@ -357,10 +358,14 @@ def thl_moe_combine_backward(m, n, topk, DY, lddy, X, ldx, rows_x, rows, weights
                                          _dt(type_dy), _dt(type_x), stream)
 
 
-def thl_gemm_w4(m, n, k, W, ldw, scales, X, ldx, C, ldc, D, ldd, alpha, beta, dtypes, epilogue=None,
-                stream=None) -> int:
+def thl_gemm_w4_workspace(n, k) -> int:
+    return _lib.thl_gemm_w4_workspace(n, k)
+
+
+def thl_gemm_w4(m, n, k, W, ldw, scales, X, ldx, C, ldc, D, ldd, alpha, beta, dtypes, epilogue=None, workspace=None,
+                workspace_bytes=0, stream=None) -> int:
     return _lib.thl_gemm_w4(m, n, k, W, ldw, _ref(scales), X, ldx, C, ldc, D, ldd, alpha, beta, _ref(dtypes),
-                            _ref(epilogue), stream)
+                            _ref(epilogue), workspace, workspace_bytes, stream)
 
 
 # Torch-tensor forms.  An array of tokens is a (tokens, features) tensor whose
@@ -620,8 +625,12 @@ def gemm_w4(w, x, d, *, scales, group, type_w="u4", zeros=None, c=None, alpha=1.
     gs = thl_group_scales(ps, lds, pz, ldz, group, ts)
     dts = thl_dtypes(DTYPES[type_w], _format(x), tc, _format(d), tb, _F32)
     epi = thl_epilogue(flags | _ACTS[act], pb, None, 0)
+    size, pws = _lib.thl_gemm_w4_workspace(n, k), 0
+    if size:
+        workspace = _torch.empty(size, dtype=_torch.uint8, device=x.device)
+        pws = workspace.data_ptr()
     _call(_lib.thl_gemm_w4, dev, m, n, k, pw, 2 * ldw, ctypes.byref(gs), px, ldx, pc, ldc, pd, ldd, alpha, beta,
-          ctypes.byref(dts), ctypes.byref(epi))
+          ctypes.byref(dts), ctypes.byref(epi), pws, size)
     return d
 
 

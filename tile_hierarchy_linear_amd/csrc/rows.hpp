@@ -81,6 +81,21 @@ __device__ __forceinline__ void to_f8(const Raw8<B>& r, bool bf, float (&v)[8]) 
   }
 }
 
+// v + v of the lane that `ctrl` (a DPP control) names.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __builtin_bit_cast(
+                 float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+// Sum over each aligned 16 lanes, in all of them: neighbours, pairs, then
+// halves of eight and of sixteen mirrored.
+__device__ __forceinline__ float sum16(float v) {
+  v = dpp_add<0xb1>(v);
+  v = dpp_add<0x4e>(v);
+  v = dpp_add<0x141>(v);
+  return dpp_add<0x140>(v);
+}
+
 // Sum of NV values over the WPR wavefronts of a workgroup (every lane gets
 // it), always in the same order.  `slot` is an LDS area of NV * WPR floats
 // that no lane of the workgroup may still be reading.
