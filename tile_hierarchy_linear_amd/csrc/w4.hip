@@ -163,7 +163,7 @@ __device__ __forceinline__ void words(const void* p, uint32_t* o) {
   }
 }
 
-// A whole unit's.
+// A whole unit's, of the lane's own feature.
 template <int WT, int GPU>
 __device__ __forceinline__ void load_groups(const W4Args& a, int64_t srow, int64_t zrow, int u, Groups<WT, GPU>& o) {
   const int first = static_cast<int>((256 * static_cast<int64_t>(u)) >> a.group_shift);
@@ -204,6 +204,15 @@ __device__ __forceinline__ void load_groups_end(const W4Args& a, int64_t srow, i
   }
 }
 
+// Lane group j's value in all four lane groups (of 16 lanes), j = 0 .. 3.
+__device__ __forceinline__ void spread(uint32_t v, uint32_t (&o)[4]) {
+  typedef unsigned v2 __attribute__((ext_vector_type(2)));
+  const v2 h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  const v2 a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+  const v2 b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+  o[0] = a[0], o[1] = a[1], o[2] = b[0], o[3] = b[1];
+}
+
 // A scale as stored (its low 8 or 16 bits) in fp32.
 template <int WT>
 __device__ __forceinline__ float scale_of(const W4Args& a, uint32_t b) {
@@ -230,13 +239,6 @@ __device__ __forceinline__ float group_offset(const Groups<WT, GPU>& o, int q) {
   return 24.0f;
 }
 
-// A whole unit's 32 bytes of one feature's codes held by a lane (bytes 16 g
-// and 64 + 16 g of its 128).
-__device__ __forceinline__ void load_codes(const uint8_t* row, int u, int g, v4i (&o)[2]) {
-  const uint8_t* p = row + 128 * static_cast<int64_t>(u) + 16 * g;
-  o[0] = *reinterpret_cast<const v4i_a1*>(p);
-  o[1] = *reinterpret_cast<const v4i_a1*>(p + 64);
-}
 // 16 bytes of codes of which `left` exist; the others read as zero.
 __device__ __forceinline__ void load_codes_at(const uint8_t* p, int64_t left, v4i& o) {
   o = v4i{0, 0, 0, 0};
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(W4Args a, int turned) {
 
 template <int WT, bool BF, int GPU, int MT, int NB>
 __global__ void __launch_bounds__(512) w4_many_kernel(W4Args a) {
-  extern __shared__ float part[];  // [wavefront][NB][MT][4][64]
+  extern __shared__ __attribute__((aligned(16))) uint8_t area[];  // the codes of a unit by wavefront, then the sums
   constexpr int LEN = 256 / GPU;
   constexpr bool TURN = LEN < 128, FOLD = WT == W_E2M1 && BF;
   constexpr int RING = MT == 4 && !FOLD ? 4 : 8;  // steps of activations on their way (registers allow)
@@ -559,31 +561,43 @@ __global__ void __launch_bounds__(512) w4_many_kernel(W4Args a) {
   const int i0 = static_cast<int>(blockIdx.x) * 16 * NB, j0 = static_cast<int>(blockIdx.y) * 16 * MT;
   const int units = static_cast<int>((static_cast<int64_t>(a.k) + 255) >> 8), whole = a.k >> 8;
 
+  // Codes are loaded along the rows, eight lanes a row's 128 bytes of a unit,
+  // and turned into operand order through LDS (in operand order neighbouring
+  // lanes hold different rows, and a load takes a cache access a lane instead
+  // of one for four).  Position p of row r holds its 16-byte chunk p ^ (r % 8),
+  // so that neither the writes nor the reads meet in a bank.
   // Features past m repeat the last one; nothing of them is stored.
-  const uint8_t* w[NB];
-  int64_t srow[NB], zrow[NB];
+  auto feature = [&](int i) { return static_cast<int64_t>(i < a.m ? i : a.m - 1); };
+  const uint8_t* w[NB][2];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int i = i0 + 16 * b + col < a.m ? i0 + 16 * b + col : a.m - 1;
-    w[b] = a.w + static_cast<int64_t>(i) * a.ldw_bytes;
-    srow[b] = static_cast<int64_t>(i) * a.ld_scales;
-    zrow[b] = static_cast<int64_t>(i) * a.ld_zeros;
-  }
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      w[b][h] = a.w + feature(i0 + 16 * b + 8 * h + (lane >> 3)) * a.ldw_bytes + 16 * (lane & 7);
+  v4i* const turned = reinterpret_cast<v4i*>(area) + wave * NB * 128;
+  const int put = (lane >> 3) * 8 + ((lane & 7) ^ (lane >> 3));  // row lane / 8 of the first eight
+  const int get = col * 8 + (g ^ (col & 7));                     // chunk g of row col (chunk 4 + g: ^ 4)
+  // Scales: lane group g asks for tile g % NB of the unit g / NB turns on,
+  // 4 / NB units at a time.
+  constexpr int UNITS = 4 / NB;
+  const int64_t gi = feature(i0 + 16 * (g % NB) + col);
+  const int64_t srow = gi * a.ld_scales, zrow = gi * a.ld_zeros;
   const v4i* x = reinterpret_cast<const v4i*>(a.packed) + fragment(blockIdx.y * MT, units, 0, 0) + lane;
 
-  struct Unit {
-    v4i w[NB][2];
-    Groups<WT, GPU> g[NB];
-  } ring[2];
+  v4i ring[2][NB][2];
   // Every load is issued whatever the position, of a unit that exists: with
   // loads behind branches the compiler waits for all of them at each use.
-  auto load = [&](int v, Unit& o) {
-    const int u = v < whole ? v : whole - 1;
+  auto load = [&](int v, v4i (&o)[NB][2]) {
+    const int64_t u = v < whole ? v : whole - 1;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      load_codes(w[b], u, g, o.w[b]);
-      load_groups<WT, GPU>(a, srow[b], zrow[b], u, o.g[b]);
-    }
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        o[b][h] = __builtin_nontemporal_load(reinterpret_cast<const v4i_a1*>(w[b][h] + 128 * u));
+  };
+  auto load_scales = [&](int v, Groups<WT, GPU>& o) {
+    const int u = v + waves * (g / NB);
+    load_groups<WT, GPU>(a, srow, zrow, u < whole ? u : whole - 1, o);
   };
   // Fragments of step s (0 .. 7) of unit u.
   v4i xa[RING][MT];
@@ -594,7 +608,8 @@ __global__ void __launch_bounds__(512) w4_many_kernel(W4Args a) {
   };
 
   v4f tot[NB][MT] = {}, acc[NB][MT] = {}, xs[MT] = {};
-  auto use = [&](int u, const Unit& o) {
+  // Unit u of this wavefront, its codes in operand order.
+  auto use = [&](int u, const v4i (&codes)[NB][2], const Groups<WT, GPU> (&groups)[NB]) {
 #pragma unroll
     for (int s8 = 0; s8 < 8; ++s8) {
       const int h = s8 >> 2, s = s8 & 3;
@@ -604,9 +619,9 @@ __global__ void __launch_bounds__(512) w4_many_kernel(W4Args a) {
       v4i (&xf)[MT] = xa[s8 % RING];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const v4i wq = TURN ? turn(o.w[b][h]) : o.w[b][h];
+        const v4i wq = TURN ? turn(codes[b][h]) : codes[b][h];
         const uint32_t c = static_cast<uint32_t>(wq[s]);
-        const v4i wf = decode<WT, BF>(c, FOLD ? group_scale<WT, GPU>(a, o.g[b], s8) : 1.0f);
+        const v4i wf = decode<WT, BF>(c, FOLD ? group_scale<WT, GPU>(a, groups[b], s8) : 1.0f);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           if constexpr (FOLD)
@@ -628,8 +643,8 @@ __global__ void __launch_bounds__(512) w4_many_kernel(W4Args a) {
         const int q = (done - 1) / LEN;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const float sv = group_scale<WT, GPU>(a, o.g[b], q);
-          const float ov = group_offset<WT, GPU>(o.g[b], q);
+          const float sv = group_scale<WT, GPU>(a, groups[b], q);
+          const float ov = group_offset<WT, GPU>(groups[b], q);
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
             leave<WT>(tot[b][t], acc[b][t], xs[t], sv, ov);
@@ -642,34 +657,84 @@ __global__ void __launch_bounds__(512) w4_many_kernel(W4Args a) {
     }
   };
 
+  auto turn_and_use = [&](int u, const v4i (&in)[NB][2], const Groups<WT, GPU> (&groups)[NB]) {
+    v4i codes[NB][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) turned[b * 128 + h * 64 + put] = in[b][h];
+    __builtin_amdgcn_wave_barrier();  // a wavefront's LDS accesses run in order
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) codes[b][h] = turned[b * 128 + (get ^ (4 * h))];
+    __builtin_amdgcn_wave_barrier();
+    use(u, codes, groups);
+  };
+
   // The wavefronts take the units in turn.  Loads return in order, so a
   // unit's weights are asked for after the activations of the unit before:
   // those then do not wait for memory.
   if (wave < whole) {
+    Groups<WT, GPU> asked;
+    load_scales(wave, asked);
     load(wave, ring[0]);
 #pragma unroll
     for (int s = 0; s < RING; ++s) fetch(wave, s, xa[s]);
     load(wave + waves, ring[1]);
-    for (int u = wave;; u += 2 * waves) {
-      use(u, ring[0]);
-      load(u + 2 * waves, ring[0]);
-      if (u + waves >= whole) break;
-      use(u + waves, ring[1]);
-      load(u + 3 * waves, ring[1]);
-      if (u + 2 * waves >= whole) break;
+    bool more = true;
+    for (int u = wave; more;) {
+      // the scales of the next UNITS units, one set of tiles a unit
+      constexpr int SW = sizeof(asked.s) / 4, ZW = sizeof(asked.z) / 4;
+      Groups<WT, GPU> groups[4];
+#pragma unroll
+      for (int q = 0; q < SW; ++q) {
+        uint32_t o[4];
+        spread(asked.s[q], o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) groups[j].s[q] = o[j];
+      }
+      if constexpr (WT == W_U4) {
+#pragma unroll
+        for (int q = 0; q < ZW; ++q) {
+          uint32_t o[4];
+          spread(asked.z[q], o);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) groups[j].z[q] = o[j];
+        }
+      }
+      load_scales(u + UNITS * waves, asked);
+#pragma unroll
+      for (int d = 0; d < UNITS; ++d) {
+        Groups<WT, GPU> mine[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) mine[b] = groups[d * NB + b];
+        turn_and_use(u, ring[d & 1], mine);
+        load(u + 2 * waves, ring[d & 1]);
+        u += waves;
+        if (u >= whole) {
+          more = false;
+          break;
+        }
+      }
     }
   }
   if (whole < units && wave == whole % waves) {  // K's partial unit
+    v4i codes[NB][2];
+    Groups<WT, GPU> groups[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      load_codes_end(a, w[b], whole, g, ring[0].w[b]);
-      load_groups_end<WT, GPU>(a, srow[b], zrow[b], whole, ring[0].g[b]);
+      const int64_t i = feature(i0 + 16 * b + col);
+      load_codes_end(a, a.w + i * a.ldw_bytes, whole, g, codes[b]);
+      load_groups_end<WT, GPU>(a, i * a.ld_scales, i * a.ld_zeros, whole, groups[b]);
     }
 #pragma unroll
     for (int s = 0; s < RING; ++s) fetch(whole, s, xa[s]);
-    use(whole, ring[0]);
+    use(whole, codes, groups);
   }
 
+  float* const part = reinterpret_cast<float*>(area);  // [wavefront][NB][MT][4][64]
+  __syncthreads();
   constexpr int TILE = NB * MT * 256;
 #pragma unroll
   for (int b = 0; b < NB; ++b)
@@ -719,7 +784,7 @@ hipError_t launch_many(W4Args& a, hipStream_t st) {
   void* args[] = {&a};
   return hipLaunchKernel(reinterpret_cast<const void*>(&w4_many_kernel<WT, BF, GPU, MT, NB>),
                          dim3(static_cast<unsigned>((a.m + 16 * NB - 1) / (16 * NB)), static_cast<unsigned>(gy)), dim3(waves * 64), args,
-                         static_cast<size_t>(waves) * NB * MT * 256 * sizeof(float), st);
+                         static_cast<size_t>(waves) * NB * (MT > 2 ? MT : 2) * 1024, st);
 }
 
 // Two feature tiles a wavefront read each activation once for both; one
