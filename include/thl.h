@@ -468,7 +468,7 @@ thl_status thl_moe_combine(int64_t m, int64_t n, int64_t topk, const void* X, in
  *   dweights[j*topk + t] = <DY(:, j), X(:, rows[j*topk + t])>, 0 without a place
  * DX and dweights may each be NULL (not wanted).  Columns of DX that no choice
  * has are left as they were.  type_x is X's and DX's.  Places must differ
- * (thl_moe_sort's do).  DX may be X exactly; no other overlap.
+ * (thl_moe_sort's do).  No output may overlap another array.
  */
 thl_status thl_moe_combine_backward(int64_t m, int64_t n, int64_t topk, const void* DY, int64_t lddy, const void* X,
                                     int64_t ldx, int64_t rows_x, const int32_t* rows, const float* weights, void* DX,

@@ -147,7 +147,7 @@ def cgrad(m=64, n=8, topk=2, dy=P[0], lddy=64, x=P[1], ldx=64, rows_x=16, rows=P
     (dict(m=-1), INVALID), (dict(n=-1), INVALID), (dict(lddy=1), INVALID), (dict(ldx=1), INVALID),
     (dict(lddx=1), INVALID), (dict(tdy="e4m3"), UNSUPPORTED), (dict(tx="i32"), UNSUPPORTED), (dict(dy=None), INVALID),
     (dict(x=None), INVALID), (dict(rows=None), INVALID), (dict(weights=None), INVALID), (dict(dx=P[4] + 1), MISALIGNED),
-    (dict(dw=P[5] + 2), MISALIGNED), (dict(dx=P[0]), INVALID), (dict(dx=P[1] + 2), INVALID),
+    (dict(dw=P[5] + 2), MISALIGNED), (dict(dx=P[0]), INVALID), (dict(dx=P[1]), INVALID),
     (dict(dx=P[1], lddx=72), INVALID), (dict(dx=P[2]), INVALID), (dict(dx=P[3]), INVALID), (dict(dw=P[0]), INVALID),
     (dict(dw=P[1]), INVALID), (dict(dw=P[4]), INVALID), (dict(dw=P[3]), INVALID), (dict(dx=None, dw=None), OK),
     (dict(n=0), OK), (dict(topk=0), OK),

@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(256) moe_gather_kernel(GatherArgs a) {
     const uint8_t* s = src + j * ld_src;
     const int32_t* places = a.rows + j * a.topk;
     if (left >= 16) {
-      const v4u_a1 v = *reinterpret_cast<const v4u_a1*>(s);
+      const v4u_a1 v = __builtin_nontemporal_load(reinterpret_cast<const v4u_a1*>(s));
       for (int c = 0; c < a.topk; ++c) {
         const int64_t p = places[c];
         if (p >= 0 && p < a.rows_y) *reinterpret_cast<v4u_a1*>(dst + p * ld_dst) = v;
@@ -219,44 +219,47 @@ struct CombineArgs {
   int32_t m, topk, lanes, x_type, y_type;
 };
 
-// `lanes` lanes take eight features each of a token's row; four of the
-// token's rows are in flight at a time.
-template <int XB>
+// `lanes` lanes take eight features each of a token's row; KB of the token's
+// rows are in flight at a time.  ONE: a workgroup has one token, whose places
+// and weights are then scalars.  Choices without a row load one that is there
+// (a load behind a branch would be waited for by itself) and are not added.
+template <int XB, int RUNS, int KB, bool ONE>
 __global__ void __launch_bounds__(256) moe_combine_kernel(CombineArgs a) {
   const int t = static_cast<int>(threadIdx.x);
-  const int per = 256 / a.lanes;
-  const int64_t e64 = 8 * (static_cast<int64_t>(blockIdx.y) * a.lanes + (t & (a.lanes - 1)));
+  const int per = ONE ? 1 : 256 / a.lanes;
+  const int64_t e64 = 8 * (static_cast<int64_t>(blockIdx.y) * (ONE ? 256 : a.lanes) + (ONE ? t : t & (a.lanes - 1)));
   if (e64 >= a.m) return;
-  const int e = static_cast<int>(e64), valid = a.m - e;
+  const int e = static_cast<int>(e64), m = a.m;
   const bool bf = a.x_type == THL_BF16;
-  for (int64_t j = static_cast<int64_t>(blockIdx.x) * per + t / a.lanes; j < a.n;
+  for (int64_t j = static_cast<int64_t>(blockIdx.x) * per + (ONE ? 0 : t / a.lanes); j < a.n;
        j += static_cast<int64_t>(gridDim.x) * per) {
     float acc[8] = {};
-    for (int c0 = 0; c0 < a.topk; c0 += 4) {
-      Raw8<XB> r[4];
-      float w[4];
-      bool on[4];
+    for (int c0 = 0; c0 < a.topk; c0 += KB) {
+      Raw8<XB> r[KB];
+      float w[KB];
+      bool on[KB];
+      int64_t last = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = c0 + i;
-        const int64_t p = c < a.topk ? a.rows[j * a.topk + c] : -1;
-        on[i] = p >= 0 && p < a.rows_x;
-        if (on[i]) {
-          r[i] = load_raw8<XB>(a.x, p * a.ldx + e, valid);
-          w[i] = a.weights ? a.weights[j * a.topk + c] : 1.0f;
-        }
+      for (int i = 0; i < KB; ++i) {
+        const int c = c0 + i < a.topk ? c0 + i : a.topk - 1;
+        const int64_t p = a.rows[j * a.topk + c];
+        on[i] = c0 + i < a.topk && p >= 0 && p < a.rows_x;
+        last = on[i] ? p : last;
+        r[i] = load_run<XB, RUNS>(a.x, last * a.ldx, e, m);
+        w[i] = a.weights ? a.weights[j * a.topk + c] : 1.0f;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < KB; ++i) {
         if (on[i]) {
           float v[8];
+          settle<XB, RUNS>(r[i], e, m);
           to_f8<XB>(r[i], bf, v);
 #pragma unroll
           for (int q = 0; q < 8; ++q) acc[q] += w[i] * v[q];
         }
       }
     }
-    store8_f(a.y, a.y_type, j * a.ldy + e, acc, valid < 8 ? valid : 8);
+    store8_f(a.y, a.y_type, j * a.ldy + e, acc, m - e < 8 ? m - e : 8);
   }
 }
 
@@ -272,42 +275,45 @@ struct CombineGradArgs {
 };
 
 // WPT wavefronts per token; KB of its choices at a time share each read of
-// dy.  XB, DB: bytes of an element of X / DX and of DY.
-template <int XB, int DB, int WPT, int KB>
+// dy.  XB, DB: bytes of an element of X / DX and of DY.  DOT: dweights is
+// wanted (X is read).  Choices without a row as in combine.
+template <int XB, int DB, int RUNS, int WPT, int KB, bool DOT>
 __global__ void __launch_bounds__(WPT * 64) moe_combine_grad_kernel(CombineGradArgs a) {
   __shared__ float red[2][KB * WPT];
-  const int t = static_cast<int>(threadIdx.x);
+  const int t = static_cast<int>(threadIdx.x), m = a.m;
   const bool x_bf = a.x_type == THL_BF16, d_bf = a.dy_type == THL_BF16;
   int parity = 0;
   for (int64_t j = blockIdx.x; j < a.n; j += gridDim.x) {
     for (int c0 = 0; c0 < a.topk; c0 += KB, parity ^= 1) {
-      int64_t place[KB];
+      int64_t place[KB], last = 0;
       float w[KB], dot[KB];
       bool on[KB];
 #pragma unroll
       for (int i = 0; i < KB; ++i) {
-        const int c = c0 + i;
-        place[i] = c < a.topk ? a.rows[j * a.topk + c] : -1;
-        on[i] = place[i] >= 0 && place[i] < a.rows_x;
-        w[i] = on[i] && a.dx ? a.weights[j * a.topk + c] : 0.0f;
+        const int c = c0 + i < a.topk ? c0 + i : a.topk - 1;
+        const int64_t p = a.rows[j * a.topk + c];
+        on[i] = c0 + i < a.topk && p >= 0 && p < a.rows_x;
+        last = on[i] ? p : last;
+        place[i] = last;
+        w[i] = a.dx ? a.weights[j * a.topk + c] : 0.0f;
         dot[i] = 0.0f;
       }
-      for (int64_t e = 8 * t; e < a.m; e += 8 * WPT * 64) {
-        const int valid = static_cast<int>(a.m - e);
-        const Raw8<DB> dr = load_raw8<DB>(a.dy, j * a.lddy + e, valid);
+      for (int e = 8 * t; e < m; e += 8 * WPT * 64) {
+        Raw8<DB> dr = load_run<DB, RUNS>(a.dy, j * a.lddy, e, m);
         Raw8<XB> xr[KB];
-        if (a.dweights) {
+        if constexpr (DOT) {
 #pragma unroll
-          for (int i = 0; i < KB; ++i)
-            if (on[i]) xr[i] = load_raw8<XB>(a.x, place[i] * a.ldx + e, valid);
+          for (int i = 0; i < KB; ++i) xr[i] = load_run<XB, RUNS>(a.x, place[i] * a.ldx, e, m);
         }
         float d[8];
+        settle<DB, RUNS>(dr, e, m);
         to_f8<DB>(dr, d_bf, d);
 #pragma unroll
         for (int i = 0; i < KB; ++i) {
           if (!on[i]) continue;
-          if (a.dweights) {
+          if constexpr (DOT) {
             float v[8];
+            settle<XB, RUNS>(xr[i], e, m);
             to_f8<XB>(xr[i], x_bf, v);
 #pragma unroll
             for (int q = 0; q < 8; ++q) dot[i] += d[q] * v[q];
@@ -316,11 +322,11 @@ __global__ void __launch_bounds__(WPT * 64) moe_combine_grad_kernel(CombineGradA
             float o[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) o[q] = w[i] * d[q];
-            store8_f(a.dx, a.x_type, place[i] * a.lddx + e, o, valid < 8 ? valid : 8);
+            store8_f(a.dx, a.x_type, place[i] * a.lddx + e, o, m - e < 8 ? m - e : 8);
           }
         }
       }
-      if (a.dweights) {
+      if constexpr (DOT) {
         row_sum<KB, WPT>(dot, red[parity]);
         if (t == 0) {
 #pragma unroll
@@ -337,6 +343,17 @@ __global__ void __launch_bounds__(WPT * 64) moe_combine_grad_kernel(CombineGradA
 hipError_t launch(const void* f, dim3 grid, int block, void* arg, hipStream_t st) {
   void* args[] = {arg};
   return hipLaunchKernel(f, grid, dim3(block), args, 0, st);
+}
+
+__global__ void __launch_bounds__(256) zeros_kernel(float* p, int64_t n) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256)
+    p[i] = 0.0f;
+}
+hipError_t launch_zeros(float* p, int64_t n, hipStream_t st) {
+  void* args[] = {&p, &n};
+  const int64_t blocks = (n + 255) / 256;
+  return hipLaunchKernel(reinterpret_cast<const void*>(&zeros_kernel),
+                         dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)), dim3(256), args, 0, st);
 }
 
 // Lanes per token for `units` pieces of work: a power of two up to 256.
@@ -356,22 +373,60 @@ bool token_grid(int64_t n, int64_t units, int lanes, dim3* g) {
   return true;
 }
 
-template <int XB, int DB, int WPT>
+// A token of up to 1,024 features goes to one wavefront, longer ones to four.
+template <int XB, int DB, int RUNS, bool DOT>
 hipError_t launch_combine_grad(CombineGradArgs& a, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(a.n < 65536 ? a.n : 65536));
-#define THL_CGRAD(KB) \
-  return launch(reinterpret_cast<const void*>(&moe_combine_grad_kernel<XB, DB, WPT, KB>), grid, WPT * 64, &a, st)
-  if (a.topk == 1) THL_CGRAD(1);
-  if (a.topk == 2) THL_CGRAD(2);
-  if (a.topk <= 4) THL_CGRAD(4);
-  THL_CGRAD(8);
+#define THL_CGRAD(WPT, KB)                                                                                         \
+  return launch(reinterpret_cast<const void*>(&moe_combine_grad_kernel<XB, DB, RUNS, WPT, KB, DOT>), grid, WPT * 64, \
+                &a, st)
+  if (a.m <= 1024) {
+    if (a.topk <= 2) THL_CGRAD(1, 2);
+    THL_CGRAD(1, 8);
+  }
+  if constexpr (RUNS != RUNS_TINY) {
+    if (a.topk <= 2) THL_CGRAD(4, 2);
+    if (a.topk <= 4) THL_CGRAD(4, 4);
+    THL_CGRAD(4, 8);
+  }
+  return hipErrorInvalidValue;
 #undef THL_CGRAD
 }
-
-// A token of up to 1,024 features goes to one wavefront, longer ones to four.
 template <int XB, int DB>
 hipError_t launch_combine_grad(CombineGradArgs& a, hipStream_t st) {
-  return a.m <= 1024 ? launch_combine_grad<XB, DB, 1>(a, st) : launch_combine_grad<XB, DB, 4>(a, st);
+  const int runs = runs_of(a.m);
+  if (a.dweights) {
+    if (runs == RUNS_TINY) return launch_combine_grad<XB, DB, RUNS_TINY, true>(a, st);
+    return runs == RUNS_WHOLE ? launch_combine_grad<XB, DB, RUNS_WHOLE, true>(a, st)
+                              : launch_combine_grad<XB, DB, RUNS_RAGGED, true>(a, st);
+  }
+  if (runs == RUNS_TINY) return launch_combine_grad<XB, DB, RUNS_TINY, false>(a, st);
+  return runs == RUNS_WHOLE ? launch_combine_grad<XB, DB, RUNS_WHOLE, false>(a, st)
+                            : launch_combine_grad<XB, DB, RUNS_RAGGED, false>(a, st);
+}
+
+template <int XB, int RUNS>
+hipError_t launch_combine(CombineArgs& a, dim3 grid, hipStream_t st) {
+#define THL_COMBINE(KB, ONE) \
+  return launch(reinterpret_cast<const void*>(&moe_combine_kernel<XB, RUNS, KB, ONE>), grid, 256, &a, st)
+  if (a.lanes == 256) {
+    if constexpr (RUNS != RUNS_TINY) {
+      if (a.topk <= 2) THL_COMBINE(2, true);
+      if (a.topk <= 4) THL_COMBINE(4, true);
+      THL_COMBINE(8, true);
+    }
+    return hipErrorInvalidValue;
+  }
+  if (a.topk <= 2) THL_COMBINE(2, false);
+  THL_COMBINE(8, false);
+#undef THL_COMBINE
+}
+template <int XB>
+hipError_t launch_combine(CombineArgs& a, dim3 grid, hipStream_t st) {
+  const int runs = runs_of(a.m);
+  if (runs == RUNS_TINY) return launch_combine<XB, RUNS_TINY>(a, grid, st);
+  return runs == RUNS_WHOLE ? launch_combine<XB, RUNS_WHOLE>(a, grid, st)
+                            : launch_combine<XB, RUNS_RAGGED>(a, grid, st);
 }
 
 bool big(int64_t v) { return v > INT32_MAX; }
@@ -512,9 +567,9 @@ thl_status thl_moe_combine(int64_t m, int64_t n, int64_t topk, const void* X, in
   a.lanes = lanes_for(units);
   dim3 grid;
   if (!token_grid(n, units, a.lanes, &grid)) return THL_ERR_UNSUPPORTED;
-  const void* f = type_x == THL_F32 ? reinterpret_cast<const void*>(&moe_combine_kernel<4>)
-                                    : reinterpret_cast<const void*>(&moe_combine_kernel<2>);
-  return launch(f, grid, 256, &a, stream) == hipSuccess ? THL_OK : THL_ERR_HIP;
+  if (rows_x == 0) a.topk = 0;  // no row to add
+  const hipError_t e = type_x == THL_F32 ? launch_combine<4>(a, grid, stream) : launch_combine<2>(a, grid, stream);
+  return e == hipSuccess ? THL_OK : THL_ERR_HIP;
 }
 
 thl_status thl_moe_combine_backward(int64_t m, int64_t n, int64_t topk, const void* DY, int64_t lddy, const void* X,
@@ -537,12 +592,16 @@ thl_status thl_moe_combine_backward(int64_t m, int64_t n, int64_t topk, const vo
   const Range rx = dweights ? matrix_range(X, type_x, m, rows_x, ldx) : Range{};
   const Range rw = DX ? vector_range(weights, n * topk, 4) : Range{};
   const Range rd = matrix_range(DX, type_x, m, rows_x, lddx), rv = vector_range(dweights, n * topk, 4);
-  // DX may be X exactly: a lane reads its features of a row before it writes them
-  if (overlaps(rd, rx) && !(DX == X && lddx == ldx)) return THL_ERR_INVALID;
+  if (overlaps(rd, rx)) return THL_ERR_INVALID;
   for (const Range& o : {rg, rr, rw})
     if (overlaps(rd, o) || overlaps(rv, o)) return THL_ERR_INVALID;
   if (overlaps(rv, rx) || overlaps(rv, rd)) return THL_ERR_INVALID;
 
+  if (rows_x == 0) {  // no row has a place
+    if (!dweights) return THL_OK;
+    const hipError_t e = launch_zeros(dweights, n * topk, stream);
+    return e == hipSuccess ? THL_OK : THL_ERR_HIP;
+  }
   CombineGradArgs a{};
   a.dy = DY, a.x = X, a.dx = DX, a.dweights = dweights, a.rows = rows, a.weights = weights;
   a.lddy = lddy, a.ldx = ldx, a.lddx = lddx, a.n = n, a.rows_x = rows_x;

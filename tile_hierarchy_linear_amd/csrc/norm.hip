@@ -87,88 +87,114 @@ __device__ __forceinline__ void store_out(const NormArgs& a, int64_t row, int e,
 
 // XB, RB: bytes of an element of X and of R / S (0: no residual).  CH = 0:
 // any number of features, read twice.
-template <int XB, int RB, int WPR, int CH>
+template <int XB, int RB, int WPR, int CH, int RUNS>
 __global__ void __launch_bounds__(WPR * 64) rmsnorm_kernel(NormArgs a) {
   constexpr int T = WPR * 64;
   __shared__ float red[2][WPR];
-  const int t = static_cast<int>(threadIdx.x);
+  const int t = static_cast<int>(threadIdx.x), m = a.m;
   const bool x_bf = a.x_type == THL_BF16, r_bf = a.r_type == THL_BF16;
   int parity = 0;
 
   // x + r of features e .. e+7
-  auto add = [&](const Raw8<XB>& x, const Raw8<RB>& r, float (&v)[8]) {
+  auto add = [&](Raw8<XB>& x, Raw8<RB>& r, int e, float (&v)[8]) {
+    settle<XB, RUNS>(x, e, m);
     to_f8<XB>(x, x_bf, v);
     if constexpr (RB != 0) {
       float u[8];
+      settle<RB, RUNS>(r, e, m);
       to_f8<RB>(r, r_bf, u);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += u[i];
     }
   };
+  auto store_sum = [&](int64_t row, int e, const float (&v)[8]) {
+    if constexpr (RB != 0) {
+      if (a.s && e < m) store8_f(a.s, a.r_type, row * a.lds + e, v, m - e < 8 ? m - e : 8);
+    }
+  };
 
   if constexpr (CH > 0) {
-    float w[CH][8];
+    RawAny wr[CH];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int e = 8 * (t + T * c), valid = a.m - e;
-      load8_f(a.w, a.w_type, e, valid < 0 ? 0 : (valid < 8 ? valid : 8), w[c]);
-    }
+    for (int c = 0; c < CH; ++c) wr[c] = load_any<RUNS>(a.w, a.w_type, 8 * (t + T * c), m);
     for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x, parity ^= 1) {
       Raw8<XB> x[CH];
       Raw8<RB> r[CH];
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int e = 8 * (t + T * c);
-        x[c] = load_raw8<XB>(a.x, row * a.ldx + e, a.m - e);
-        r[c] = load_raw8<RB>(a.r, row * a.ldr + e, a.m - e);
+        x[c] = load_run<XB, RUNS>(a.x, row * a.ldx, 8 * (t + T * c), m);
+        r[c] = load_run<RB, RUNS>(a.r, row * a.ldr, 8 * (t + T * c), m);
       }
       float v[CH][8], ss[1] = {0.0f};
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        add(x[c], r[c], v[c]);
+        add(x[c], r[c], 8 * (t + T * c), v[c]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss[0] += v[c][i] * v[c][i];
-        if constexpr (RB != 0) {
-          const int e = 8 * (t + T * c), valid = a.m - e;
-          if (a.s && valid > 0) store8_f(a.s, a.r_type, row * a.lds + e, v[c], valid < 8 ? valid : 8);
-        }
       }
+      // Past this sum every lane has read its run: with ragged runs the last
+      // two overlap, and S may be stored over X or R.
       row_sum<1, WPR>(ss, red[parity]);
-      const float rho = rsqrtf(ss[0] / static_cast<float>(a.m) + a.eps);
+      const float rho = rsqrtf(ss[0] / static_cast<float>(m) + a.eps);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        float o[8];
+        const int e = 8 * (t + T * c);
+        store_sum(row, e, v[c]);
+        float w[8], o[8];
+        any_f8<RUNS>(wr[c], a.w_type, e, m, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = v[c][i] * rho * w[c][i];
-        store_out(a, row, 8 * (t + T * c), o);
+        for (int i = 0; i < 8; ++i) o[i] = v[c][i] * rho * w[i];
+        store_out(a, row, e, o);
       }
     }
   } else {
-    // S may be R or X, and Y may be X: the second pass reads an element
-    // before the same lane overwrites it.
+    // S may be X or R, and Y may be X: the second pass reads an element
+    // before the same lane overwrites it, and no lane reads another's (whole
+    // runs, or element by element in the last one).
+    auto run = [&](int64_t row, int e, float (&v)[8]) {
+      if (RUNS == RUNS_WHOLE || e + 8 <= m) {
+        Raw8<XB> x = load_run<XB, RUNS_WHOLE>(a.x, row * a.ldx, e, m);
+        Raw8<RB> r = load_run<RB, RUNS_WHOLE>(a.r, row * a.ldr, e, m);
+        to_f8<XB>(x, x_bf, v);
+        if constexpr (RB != 0) {
+          float u[8];
+          to_f8<RB>(r, r_bf, u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += u[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] = 0.0f;
+          if (e + i < m) {
+            v[i] = load_f(a.x, a.x_type, row * a.ldx + e + i);
+            if constexpr (RB != 0) v[i] += load_f(a.r, a.r_type, row * a.ldr + e + i);
+          }
+        }
+      }
+    };
     for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x, parity ^= 1) {
       float ss[1] = {0.0f};
-      for (int64_t e = 8 * t; e < a.m; e += 8 * T) {
-        const int valid = static_cast<int>(a.m - e);
+      for (int e = 8 * t; e < m; e += 8 * T) {
         float v[8];
-        add(load_raw8<XB>(a.x, row * a.ldx + e, valid), load_raw8<RB>(a.r, row * a.ldr + e, valid), v);
+        run(row, e, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss[0] += v[i] * v[i];
       }
       row_sum<1, WPR>(ss, red[parity]);
-      const float rho = rsqrtf(ss[0] / static_cast<float>(a.m) + a.eps);
+      const float rho = rsqrtf(ss[0] / static_cast<float>(m) + a.eps);
       // whole groups of four lanes stay together for the block maximum
-      for (int64_t e = 8 * t; (e & ~INT64_C(31)) < a.m; e += 8 * T) {
-        const int valid = static_cast<int>(a.m - e);
-        float v[8], w[8];
-        add(load_raw8<XB>(a.x, row * a.ldx + e, valid), load_raw8<RB>(a.r, row * a.ldr + e, valid), v);
-        load8_f(a.w, a.w_type, e, valid < 0 ? 0 : (valid < 8 ? valid : 8), w);
-        if constexpr (RB != 0) {
-          if (a.s && valid > 0) store8_f(a.s, a.r_type, row * a.lds + e, v, valid < 8 ? valid : 8);
+      for (int e = 8 * t; (e & ~31) < m; e += 8 * T) {
+        const int valid = m - e;
+        float v[8] = {}, w[8] = {};
+        if (valid > 0) {
+          run(row, e, v);
+          load8_f(a.w, a.w_type, e, valid < 8 ? valid : 8, w);
         }
+        store_sum(row, e, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = v[i] * rho * w[i];
-        store_out(a, row, static_cast<int>(e), v);
+        store_out(a, row, e, v);
       }
     }
   }
@@ -192,72 +218,77 @@ struct NormGradArgs {
 
 // SB, GB: bytes of an element of S and of the gradients.  CH = 0: any number
 // of features; dw then accumulates in the workgroup's row of `part`.
-template <int SB, int GB, int WPR, int CH>
+template <int SB, int GB, int WPR, int CH, int RUNS>
 __global__ void __launch_bounds__(WPR * 64) rmsnorm_grad_kernel(NormGradArgs a) {
   constexpr int T = WPR * 64;
   constexpr int NC = CH > 0 ? CH : 1;
   __shared__ float red[2][2 * WPR];
-  const int t = static_cast<int>(threadIdx.x);
+  const int t = static_cast<int>(threadIdx.x), m = a.m;
   const bool s_bf = a.s_type == THL_BF16, g_bf = a.g_type == THL_BF16;
   int parity = 0;
 
-  // dx of features e .. e+7, with h = rho * s and mean = mean(w * dy * h);
-  // dw's terms of this token in h
-  auto emit = [&](int64_t row, int64_t e, int valid, const float (&s)[8], const float (&g)[8], const float (&w)[8],
-                  const Raw8<GB>& dr, float rho, float mean, float (&h)[8]) {
-    float d[8];
-    if (a.dr) {
-      to_f8<GB>(dr, g_bf, d);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] = 0.0f;
-    }
+  // dx of features e .. e+7 (d: the gradient past the norm), with h = rho * s
+  // and mean = mean(w * dy * h); dw's terms of this token in h
+  auto emit = [&](int64_t row, int e, const float (&s)[8], const float (&g)[8], const float (&w)[8], float (&d)[8],
+                  float rho, float mean, float (&h)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       h[i] = s[i] * rho;
       d[i] += rho * (w[i] * g[i] - h[i] * mean);
       h[i] *= g[i];
     }
-    if (valid > 0) store8_f(a.dx, a.g_type, row * a.lddx + e, d, valid < 8 ? valid : 8);
+    if (e < m) store8_f(a.dx, a.g_type, row * a.lddx + e, d, m - e < 8 ? m - e : 8);
   };
 
-  float* part = a.part ? a.part + static_cast<int64_t>(blockIdx.x) * a.m : nullptr;
+  float* part = a.part ? a.part + static_cast<int64_t>(blockIdx.x) * m : nullptr;
   if constexpr (CH > 0) {
-    float w[NC][8], acc[NC][8] = {};
+    RawAny wr[NC];
+    float acc[NC][8] = {};
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int e = 8 * (t + T * c), valid = a.m - e;
-      load8_f(a.w, a.w_type, e, valid < 0 ? 0 : (valid < 8 ? valid : 8), w[c]);
-    }
+    for (int c = 0; c < NC; ++c) wr[c] = load_any<RUNS>(a.w, a.w_type, 8 * (t + T * c), m);
+    // without a gradient past the norm, dy is loaded in its place and not used
+    const void* dr = a.dr ? a.dr : a.dy;
+    const int64_t lddr = a.dr ? a.lddr : a.lddy;
     for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x, parity ^= 1) {
       Raw8<SB> sr[NC];
-      Raw8<GB> gr[NC], dr[NC];
+      Raw8<GB> gr[NC], rr[NC];
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int e = 8 * (t + T * c);
-        sr[c] = load_raw8<SB>(a.s, row * a.lds + e, a.m - e);
-        gr[c] = load_raw8<GB>(a.dy, row * a.lddy + e, a.m - e);
-        if (a.dr) dr[c] = load_raw8<GB>(a.dr, row * a.lddr + e, a.m - e);
+        sr[c] = load_run<SB, RUNS>(a.s, row * a.lds, e, m);
+        gr[c] = load_run<GB, RUNS>(a.dy, row * a.lddy, e, m);
+        rr[c] = load_run<GB, RUNS>(dr, row * lddr, e, m);
       }
-      float s[NC][8], g[NC][8], sum[2] = {0.0f, 0.0f};
+      float s[NC][8], g[NC][8], w[NC][8], sum[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
+        const int e = 8 * (t + T * c);
+        settle<SB, RUNS>(sr[c], e, m);
+        settle<GB, RUNS>(gr[c], e, m);
         to_f8<SB>(sr[c], s_bf, s[c]);
         to_f8<GB>(gr[c], g_bf, g[c]);
+        any_f8<RUNS>(wr[c], a.w_type, e, m, w[c]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           sum[0] += s[c][i] * s[c][i];
           sum[1] += w[c][i] * g[c][i] * s[c][i];
         }
+        settle<GB, RUNS>(rr[c], e, m);
+      }
+      // Past these sums every lane has read its runs (dx may be stored over
+      // any of them).
+      if constexpr (RUNS == RUNS_RAGGED) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) arrived(rr[c]);
       }
       row_sum<2, WPR>(sum, red[parity]);
-      const float rho = rsqrtf(sum[0] / static_cast<float>(a.m) + a.eps);
-      const float mean = rho * sum[1] / static_cast<float>(a.m);
+      const float rho = rsqrtf(sum[0] / static_cast<float>(m) + a.eps);
+      const float mean = rho * sum[1] / static_cast<float>(m);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int e = 8 * (t + T * c);
-        float h[8];
-        emit(row, e, a.m - e, s[c], g[c], w[c], dr[c], rho, mean, h);
+        float d[8] = {}, h[8];
+        if (a.dr) to_f8<GB>(rr[c], g_bf, d);
+        emit(row, 8 * (t + T * c), s[c], g[c], w[c], d, rho, mean, h);
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[c][i] += h[i];
       }
@@ -265,19 +296,19 @@ __global__ void __launch_bounds__(WPR * 64) rmsnorm_grad_kernel(NormGradArgs a) 
     if (part) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int e = 8 * (t + T * c), valid = a.m - e;
-        if (valid > 0) store8_f(part, THL_F32, e, acc[c], valid < 8 ? valid : 8);
+        const int e = 8 * (t + T * c);
+        if (e < m) store8_f(part, THL_F32, e, acc[c], m - e < 8 ? m - e : 8);
       }
     }
   } else {
     for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x, parity ^= 1) {
       float sum[2] = {0.0f, 0.0f};
-      for (int64_t e = 8 * t; e < a.m; e += 8 * T) {
-        const int valid = static_cast<int>(a.m - e);
+      for (int e = 8 * t; e < m; e += 8 * T) {
+        const int k = m - e < 8 ? m - e : 8;
         float s[8], g[8], w[8];
-        to_f8<SB>(load_raw8<SB>(a.s, row * a.lds + e, valid), s_bf, s);
-        to_f8<GB>(load_raw8<GB>(a.dy, row * a.lddy + e, valid), g_bf, g);
-        load8_f(a.w, a.w_type, e, valid < 8 ? valid : 8, w);
+        load8_f(a.s, a.s_type, row * a.lds + e, k, s);
+        load8_f(a.dy, a.g_type, row * a.lddy + e, k, g);
+        load8_f(a.w, a.w_type, e, k, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           sum[0] += s[i] * s[i];
@@ -285,17 +316,16 @@ __global__ void __launch_bounds__(WPR * 64) rmsnorm_grad_kernel(NormGradArgs a) 
         }
       }
       row_sum<2, WPR>(sum, red[parity]);
-      const float rho = rsqrtf(sum[0] / static_cast<float>(a.m) + a.eps);
-      const float mean = rho * sum[1] / static_cast<float>(a.m);
-      for (int64_t e = 8 * t; e < a.m; e += 8 * T) {
-        const int valid = static_cast<int>(a.m - e), k = valid < 8 ? valid : 8;
-        float s[8], g[8], w[8], h[8];
-        to_f8<SB>(load_raw8<SB>(a.s, row * a.lds + e, valid), s_bf, s);
-        to_f8<GB>(load_raw8<GB>(a.dy, row * a.lddy + e, valid), g_bf, g);
+      const float rho = rsqrtf(sum[0] / static_cast<float>(m) + a.eps);
+      const float mean = rho * sum[1] / static_cast<float>(m);
+      for (int e = 8 * t; e < m; e += 8 * T) {
+        const int k = m - e < 8 ? m - e : 8;
+        float s[8], g[8], w[8], d[8] = {}, h[8];
+        load8_f(a.s, a.s_type, row * a.lds + e, k, s);
+        load8_f(a.dy, a.g_type, row * a.lddy + e, k, g);
         load8_f(a.w, a.w_type, e, k, w);
-        Raw8<GB> dr;
-        if (a.dr) dr = load_raw8<GB>(a.dr, row * a.lddr + e, valid);
-        emit(row, e, valid, s, g, w, dr, rho, mean, h);
+        if (a.dr) load8_f(a.dr, a.g_type, row * a.lddr + e, k, d);
+        emit(row, e, s, g, w, d, rho, mean, h);
         if (part) {  // this lane's own features of the workgroup's own row
           float p[8];
           if (row >= gridDim.x) {
@@ -347,35 +377,61 @@ int64_t norm_grid(int64_t n, int wpr) {
   return n < most ? n : most;
 }
 
+// A token goes to as few wavefronts as hold it at 32 features a lane where
+// there are tokens to fill the device, and to as many as hold it at 8 or 16
+// where there are not: one token of 8,192 takes 7.4 us on four wavefronts.
+template <int XB, int RB, int RUNS>
+hipError_t launch_norm(NormArgs& a, hipStream_t st) {
+#define THL_NORM(WPR, CH)                                                                                            \
+  return launch(reinterpret_cast<const void*>(&rmsnorm_kernel<XB, RB, WPR, CH, RUNS>), norm_grid(a.n, WPR), WPR * 64, \
+                &a, st)
+  const bool few = a.n <= 1024;
+  if (a.m <= 512) THL_NORM(1, 1);
+  if constexpr (RUNS != RUNS_TINY) {
+    if (a.m <= 1024) THL_NORM(1, 2);
+    if (a.m <= 2048) THL_NORM(4, 1);
+    if (few && a.m <= 4096) THL_NORM(8, 1);
+    if (few && a.m <= 8192) THL_NORM(16, 1);
+    if (a.m <= 4096) THL_NORM(4, 2);
+    if (a.m <= 8192) THL_NORM(4, 4);
+    if (a.m <= 16384) THL_NORM(16, 2);
+    THL_NORM(16, 0);
+  }
+  return hipErrorInvalidValue;
+#undef THL_NORM
+}
 template <int XB, int RB>
 hipError_t launch_norm(NormArgs& a, hipStream_t st) {
-#define THL_NORM(WPR, CH) \
-  return launch(reinterpret_cast<const void*>(&rmsnorm_kernel<XB, RB, WPR, CH>), norm_grid(a.n, WPR), WPR * 64, &a, st)
-  if (a.m <= 512) THL_NORM(1, 1);
-  if (a.m <= 1024) THL_NORM(1, 2);
-  if (a.m <= 2048) THL_NORM(4, 1);
-  if (a.m <= 4096) THL_NORM(4, 2);
-  if (a.m <= 8192) THL_NORM(4, 4);
-  if (a.m <= 16384) THL_NORM(16, 2);
-  THL_NORM(16, 0);
-#undef THL_NORM
+  const int runs = runs_of(a.m);
+  if (runs == RUNS_TINY) return launch_norm<XB, RB, RUNS_TINY>(a, st);
+  return runs == RUNS_WHOLE ? launch_norm<XB, RB, RUNS_WHOLE>(a, st) : launch_norm<XB, RB, RUNS_RAGGED>(a, st);
 }
 
 // Workgroups of the gradient, and rows of partial dw: enough to fill the
 // device, few enough that the partial rows stay a small part of the traffic.
 constexpr int kGradRows = 512;
 
-template <int SB, int GB>
+template <int SB, int GB, int RUNS>
 hipError_t launch_grad(NormGradArgs& a, int64_t grid, hipStream_t st) {
 #define THL_GRAD(WPR, CH) \
-  return launch(reinterpret_cast<const void*>(&rmsnorm_grad_kernel<SB, GB, WPR, CH>), grid, WPR * 64, &a, st)
+  return launch(reinterpret_cast<const void*>(&rmsnorm_grad_kernel<SB, GB, WPR, CH, RUNS>), grid, WPR * 64, &a, st)
   if (a.m <= 512) THL_GRAD(1, 1);
-  if (a.m <= 2048) THL_GRAD(4, 1);
-  if (a.m <= 4096) THL_GRAD(8, 1);
-  if (a.m <= 8192) THL_GRAD(16, 1);
-  if (a.m <= 16384) THL_GRAD(16, 2);
-  THL_GRAD(16, 0);
+  if constexpr (RUNS != RUNS_TINY) {
+    if (a.m <= 2048) THL_GRAD(4, 1);
+    if (a.m <= 4096) THL_GRAD(8, 1);
+    if (a.m <= 8192) THL_GRAD(16, 1);
+    if (a.m <= 16384) THL_GRAD(16, 2);
+    THL_GRAD(16, 0);
+  }
+  return hipErrorInvalidValue;
 #undef THL_GRAD
+}
+template <int SB, int GB>
+hipError_t launch_grad(NormGradArgs& a, int64_t grid, hipStream_t st) {
+  const int runs = runs_of(a.m);
+  if (runs == RUNS_TINY) return launch_grad<SB, GB, RUNS_TINY>(a, grid, st);
+  return runs == RUNS_WHOLE ? launch_grad<SB, GB, RUNS_WHOLE>(a, grid, st)
+                            : launch_grad<SB, GB, RUNS_RAGGED>(a, grid, st);
 }
 
 bool bad_ld(int64_t ld, int64_t m) { return ld < (m > 1 ? m : 1); }

@@ -126,6 +126,16 @@ __device__ __forceinline__ v4i in_order(v4i x) {
   }
 }
 
+// Eight activations of which the first `valid` exist, the others zero.
+__device__ __forceinline__ v4i load_x8(const uint16_t* p, int valid) {
+  if (valid >= 8) return *reinterpret_cast<const v4i_a2*>(p);
+  uint32_t u[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < valid) u[e / 2] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
+  return v4i{static_cast<int>(u[0]), static_cast<int>(u[1]), static_cast<int>(u[2]), static_cast<int>(u[3])};
+}
+
 // Lane group g (of 16 lanes), register s  <->  lane group s, register g.
 __device__ __forceinline__ v4i turn(v4i w) {
   typedef unsigned v2 __attribute__((ext_vector_type(2)));
@@ -378,7 +388,7 @@ __global__ void __launch_bounds__(kOneWaves * 64) w4_one_kernel(W4Args a, int ks
       xs[t] = 0.0f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const Raw8<2> r = load_raw8<2>(a.x, at + 8 * q, piece < pieces ? 8 : 0);
+        const Raw8<2> r{load_x8(a.x + at + 8 * q, piece < pieces ? 8 : 0)};
         const v4i o = in_order<WT>(r.w);
 #pragma unroll
         for (int d = 0; d < 4; ++d) x[t][4 * q + d] = o[d];
@@ -542,7 +552,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(W4Args a, int turned) {
     const int p = static_cast<int>(threadIdx.x) + 256 * q, kp = p & 31, row = p >> 5;
     const int64_t k0 = 256 * u + 8 * kp, j = 16 * tile + 4 * (row & 3) + (row >> 2);
     v4i x = {0, 0, 0, 0};
-    if (j < a.n && k0 < a.k) x = load_raw8<2>(a.x, j * a.ldx + k0, a.k - k0 < 8 ? static_cast<int>(a.k - k0) : 8).w;
+    if (j < a.n && k0 < a.k) x = load_x8(a.x + j * a.ldx + k0, a.k - k0 < 8 ? static_cast<int>(a.k - k0) : 8);
     const int h = kp >> 4, hi = (kp >> 2) & 3, lo = kp & 3;
     out[fragment(tile, units, u, 4 * h + (turned ? hi : lo)) + 16 * (turned ? lo : hi) + row] = in_order<WT>(x);
   }
