@@ -35,8 +35,9 @@ namespace {
 constexpr int kSortWaves = 8;
 constexpr int kSortThreads = kSortWaves * 64;
 constexpr int kSortBlocks = 256;
-constexpr int kMaxExperts = 1024;  // counts of eight wavefronts in 32 KB of LDS
+constexpr int kMaxExperts = 1024;   // counts of eight wavefronts in 32 KB of LDS
 constexpr int64_t kSortOne = 4096;  // entries one workgroup takes alone
+constexpr int64_t kSortChunk = 1024;  // entries at least per workgroup otherwise
 
 struct SortArgs {
   const void* ids;
@@ -49,10 +50,24 @@ struct SortArgs {
   int32_t* counts;  // blocks x experts, more than one workgroup only
 };
 
-__device__ __forceinline__ int expert_of(const SortArgs& a, int f) {
-  const int64_t at = static_cast<int64_t>(f / a.topk) * a.ld_ids + f % a.topk;
-  const int64_t id = a.ids_bytes == 8 ? static_cast<const int64_t*>(a.ids)[at] : static_cast<const int32_t*>(a.ids)[at];
-  return id >= 0 && id < a.experts ? static_cast<int>(id) : -1;
+// The experts of entries f, f + step, .. (four of them), -1 for one that is
+// dropped or lies past `end`; the loads go out together.
+__device__ __forceinline__ void experts_of(const SortArgs& a, int f, int step, int end, int (&e)[4]) {
+  int64_t id[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = f + i * step < end ? f + i * step : end - 1;
+    const int64_t k = a.ld_ids == a.topk ? at : static_cast<int64_t>(at / a.topk) * a.ld_ids + at % a.topk;
+    // the low and the high half of a 64-bit id (of a 32-bit one the same word)
+    const int32_t* p = static_cast<const int32_t*>(a.ids) + (a.ids_bytes == 8 ? 2 * k : k);
+    const int32_t lo = p[0], hi = p[a.ids_bytes == 8 ? 1 : 0];
+    id[i] = a.ids_bytes == 8 ? static_cast<int64_t>((static_cast<uint64_t>(static_cast<uint32_t>(hi)) << 32) |
+                                                    static_cast<uint32_t>(lo))
+                             : lo;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    e[i] = f + i * step < end && id[i] >= 0 && id[i] < a.experts ? static_cast<int>(id[i]) : -1;
 }
 
 __global__ void __launch_bounds__(kSortThreads) sort_count(SortArgs a) {
@@ -62,9 +77,12 @@ __global__ void __launch_bounds__(kSortThreads) sort_count(SortArgs a) {
   __syncthreads();
   const int lo = static_cast<int>(blockIdx.x) * a.chunk;
   const int hi = a.total - lo < a.chunk ? a.total : lo + a.chunk;
-  for (int f = lo + t; f < hi; f += kSortThreads) {
-    const int e = expert_of(a, f);
-    if (e >= 0) atomicAdd(&count[e], 1);
+  for (int f = lo + t; f < hi; f += 4 * kSortThreads) {
+    int e[4];
+    experts_of(a, f, kSortThreads, hi, e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (e[i] >= 0) atomicAdd(&count[e[i]], 1);
   }
   __syncthreads();
   for (int e = t; e < a.experts; e += kSortThreads)
@@ -73,41 +91,62 @@ __global__ void __launch_bounds__(kSortThreads) sort_count(SortArgs a) {
 
 __global__ void __launch_bounds__(kSortThreads) sort_place(SortArgs a) {
   __shared__ int next[kSortWaves][kMaxExperts];  // counts, then the next place, per wavefront and expert
+  __shared__ int all[kMaxExperts], before[kMaxExperts];  // entries of an expert: all, and in earlier workgroups
   __shared__ int wave_sum[kSortWaves];
   const int t = static_cast<int>(threadIdx.x), lane = t & 63, wave = t >> 6;
   const int me = static_cast<int>(blockIdx.x);
-  for (int e = t; e < a.experts; e += kSortThreads)
+  for (int e = t; e < a.experts; e += kSortThreads) {
     for (int w = 0; w < kSortWaves; ++w) next[w][e] = 0;
+    all[e] = 0;
+    before[e] = 0;
+  }
   __syncthreads();
 
   // this wavefront's segment of this workgroup's chunk
   const int lo = me * a.chunk, hi = a.total - lo < a.chunk ? a.total : lo + a.chunk;
   const int seg = ((hi - lo + kSortWaves - 1) / kSortWaves + 63) & ~63;
   const int s0 = lo + wave * seg < hi ? lo + wave * seg : hi, s1 = hi - s0 < seg ? hi : s0 + seg;
-  for (int f = s0 + lane; f < s1; f += 64) {
-    const int e = expert_of(a, f);
-    if (e >= 0) atomicAdd(&next[wave][e], 1);
+  int first[4] = {-1, -1, -1, -1};  // the segment's first four runs of 64, kept for the second pass
+  for (int f = s0; f < s1; f += 256) {
+    int e[4];
+    experts_of(a, f + lane, 64, s1, e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (f == s0) first[i] = e[i];
+      if (e[i] >= 0) atomicAdd(&next[wave][e[i]], 1);
+    }
+  }
+  if (a.blocks > 1) {
+    const int n = a.blocks * a.experts;
+    for (int i = t; i < n; i += 4 * kSortThreads) {
+      int c[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) c[q] = a.counts[i + q * kSortThreads < n ? i + q * kSortThreads : n - 1];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int at = i + q * kSortThreads, b = at / a.experts, e = at - b * a.experts;
+        if (at < n && c[q] != 0) {
+          atomicAdd(&all[e], c[q]);
+          if (b < me) atomicAdd(&before[e], c[q]);
+        }
+      }
+    }
   }
   __syncthreads();
 
-  // experts 2t, 2t+1: all their entries, and those in earlier workgroups
-  int all[2] = {0, 0}, before[2] = {0, 0};
+  // experts 2t, 2t+1: exclusive sum over the experts
+  int mine[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int e = 2 * t + i;
     if (e >= a.experts) continue;
-    if (a.blocks == 1) {
-      for (int w = 0; w < kSortWaves; ++w) all[i] += next[w][e];
+    if (a.blocks > 1) {
+      mine[i] = all[e];
     } else {
-      for (int b = 0; b < a.blocks; ++b) {
-        const int c = a.counts[static_cast<int64_t>(b) * a.experts + e];
-        all[i] += c;
-        before[i] += b < me ? c : 0;
-      }
+      for (int w = 0; w < kSortWaves; ++w) mine[i] += next[w][e];
     }
   }
-  // exclusive sum over the experts
-  int run = all[0] + all[1];
+  int run = mine[0] + mine[1];
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
     const int o = __shfl_up(run, d);
@@ -115,7 +154,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(SortArgs a) {
   }
   if (lane == 63) wave_sum[wave] = run;
   __syncthreads();
-  int start = run - all[0] - all[1];
+  int start = run - mine[0] - mine[1];
   for (int w = 0; w < wave; ++w) start += wave_sum[w];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -123,39 +162,48 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(SortArgs a) {
     if (e < a.experts) {
       if (me == 0) {
         a.offsets[e] = start;
-        if (e == a.experts - 1) a.offsets[a.experts] = start + all[i];
+        if (e == a.experts - 1) a.offsets[a.experts] = start + mine[i];
       }
-      int p = start + before[i];
+      int p = start + before[e];
       for (int w = 0; w < kSortWaves; ++w) {
         const int c = next[w][e];
         next[w][e] = p;
         p += c;
       }
-      start += all[i];
+      start += mine[i];
     }
   }
   __syncthreads();
 
   // places: lanes with one expert take consecutive ones, in lane order
   const int bits = 32 - __builtin_clz(static_cast<unsigned>(a.experts));
-  for (int f0 = s0; f0 < s1; f0 += 64) {
-    const int f = f0 + lane;
-    const int e = f < s1 ? expert_of(a, f) : -1;
-    uint64_t same = __ballot(e >= 0);
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t set = __ballot((e >> b) & 1);
-      same &= ((e >> b) & 1) ? set : ~set;
+  for (int f = s0; f < s1; f += 256) {
+    int es[4];
+    if (f == s0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) es[i] = first[i];
+    } else {
+      experts_of(a, f + lane, 64, s1, es);
     }
-    if (e >= 0) {
-      const int rank = __popcll(same & ((1ull << lane) - 1ull));
-      const int leader = __ffsll(static_cast<unsigned long long>(same)) - 1;
-      int base = 0;
-      if (rank == 0) base = atomicAdd(&next[wave][e], __popcll(same));
-      const int place = __shfl(base, leader) + rank;
-      a.rows[f] = place;
-      if (a.order) a.order[place] = f;
-    } else if (f < s1) {
-      a.rows[f] = -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = es[i], at = f + 64 * i + lane;
+      uint64_t same = __ballot(e >= 0);
+      for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __ballot((e >> b) & 1);
+        same &= ((e >> b) & 1) ? set : ~set;
+      }
+      if (e >= 0) {
+        const int rank = __popcll(same & ((1ull << lane) - 1ull));
+        const int leader = __ffsll(static_cast<unsigned long long>(same)) - 1;
+        int base = 0;
+        if (rank == 0) base = atomicAdd(&next[wave][e], __popcll(same));
+        const int place = __shfl(base, leader) + rank;
+        a.rows[at] = place;
+        if (a.order) a.order[place] = at;
+      } else if (at < s1) {
+        a.rows[at] = -1;
+      }
     }
   }
 }
@@ -447,8 +495,7 @@ void sort_split(int64_t total, int32_t* blocks, int32_t* chunk) {
   int64_t c = kSortOne;
   if (total > kSortOne) {
     c = (total + kSortBlocks - 1) / kSortBlocks;
-    c = (c + kSortThreads - 1) / kSortThreads * kSortThreads;
-    if (c < kSortOne) c = kSortOne;
+    c = c < kSortChunk ? kSortChunk : (c + kSortThreads - 1) / kSortThreads * kSortThreads;
   }
   *chunk = static_cast<int32_t>(c);
   *blocks = static_cast<int32_t>((total + c - 1) / c);

@@ -348,8 +348,14 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_reduce(const float* part, i
   const int col = static_cast<int>(threadIdx.x) & 31, sl = static_cast<int>(threadIdx.x) >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + col;
   float t = 0.0f;
-  if (c < m)
-    for (int r = sl; r < rows; r += 32) t += part[static_cast<int64_t>(r) * m + c];
+  const int64_t cc = c < m ? c : m - 1;
+  for (int r = sl; r < rows; r += 8 * 32) {  // eight loads at a time, of rows that exist
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = part[static_cast<int64_t>(r + 32 * i < rows ? r + 32 * i : r) * m + cc];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += r + 32 * i < rows ? v[i] : 0.0f;
+  }
   slice[sl][col] = t;
   __syncthreads();
   if (sl != 0 || c >= m) return;
@@ -393,6 +399,7 @@ hipError_t launch_norm(NormArgs& a, hipStream_t st) {
     if (few && a.m <= 4096) THL_NORM(8, 1);
     if (few && a.m <= 8192) THL_NORM(16, 1);
     if (a.m <= 4096) THL_NORM(4, 2);
+    if (a.m <= 6144) THL_NORM(4, 3);
     if (a.m <= 8192) THL_NORM(4, 4);
     if (a.m <= 16384) THL_NORM(16, 2);
     THL_NORM(16, 0);
