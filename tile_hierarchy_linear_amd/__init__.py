@@ -66,16 +66,18 @@ class thl_group_scales(ctypes.Structure):
                 ("ld_zeros", ctypes.c_int64), ("group", ctypes.c_int64), ("type", ctypes.c_int)]
 
 
+try:
+    import torch as _torch
+except ImportError:
+    _torch = None
+
+
 def _load():
     # One HIP runtime per process.  torch ships its own libamdhip64 and asks
     # for it by its unversioned name, so loading libthl first (which pulls in
     # the system libamdhip64.so.7) would leave two runtimes in the process and
     # device pointers from one invalid in the other.  Importing torch first
-    # makes libthl bind to torch's runtime.
-    try:
-        import torch  # noqa: F401
-    except ImportError:
-        pass
+    # (above) makes libthl bind to torch's runtime.
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run __graft_entry__.build() "
                           "or python tile_hierarchy_linear_amd/build.py")
@@ -373,264 +375,73 @@ def thl_gemm_w4(m, n, k, W, ldw, scales, X, ldx, C, ldc, D, ldd, alpha, beta, dt
 # caller made, so that serving loops and graphs reuse them.  They issue on the
 # current stream of the tensors' device, take their workspaces from torch on
 # that stream, and raise ValueError for a tensor of the wrong shape, type or
-# device and ThlError for what the library refuses.
-#
-# A small call's time is its host time: about 4 us of HIP launch, and what
-# these functions add.  So a tensor is looked at once, with the accessors that
-# build no Python object (get_device() rather than device), and the stream is
-# read as its address (0.1 us; a torch.cuda.Stream object takes 2.8).
+# device and ThlError for what the library refuses.  The tensors are read and
+# checked in csrc/torch_ops.cpp: in Python that took as long as the launch.
 
-try:
-    import torch as _torch
-
-    _FORMATS = {_torch.float32: DTYPES["f32"], _torch.float16: DTYPES["f16"], _torch.bfloat16: DTYPES["bf16"],
-                _torch.int8: DTYPES["i8"], _torch.uint8: DTYPES["i8"], _torch.int32: DTYPES["i32"],
-                _torch.float8_e4m3fn: DTYPES["e4m3"], _torch.float8_e5m2: DTYPES["e5m2"],
-                _torch.float8_e8m0fnu: DTYPES["e8m0"]}
-except ImportError:
-    pass
-_NONE, _F32, _E2M1, _E8M0 = DTYPES["none"], DTYPES["f32"], DTYPES["e2m1"], DTYPES["e8m0"]
-
-
-def _format(t) -> int:
-    f = _FORMATS.get(t.dtype)
-    if f is None:
-        raise ValueError(f"no format for tensors of {t.dtype}")
-    return f
-
-
-def _device(t) -> int:
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError("a (tokens, features) tensor on a GPU is expected first")
-    return t.get_device()
-
-
-def _tokens(what, t, dev, n, m):
-    """A (n, m) tensor's address and leading dimension."""
-    if t.shape != (n, m) or t.get_device() != dev:
-        raise ValueError(f"{what}: {tuple(t.shape)} on {t.device}, expected ({n}, {m}) on cuda:{dev}")
-    ld, step = t.stride()
-    if step != 1 and m > 1:
-        raise ValueError(f"{what}: features must be contiguous")
-    return t.data_ptr(), ld if n > 1 else max(ld, m, 1)
-
-
-def _flat(what, t, dev, shape, dtype=None):
-    """A contiguous tensor's address."""
-    if t.shape != shape or t.get_device() != dev or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{what}: {tuple(t.shape)} {t.dtype} on {t.device}, expected contiguous {tuple(shape)} "
-                         f"{dtype or ''} on cuda:{dev}")
-    return t.data_ptr()
-
-
-def _scale_bytes(what, t, dev, n, blocks):
-    """The address and leading dimension of n rows of at least `blocks` bytes."""
-    if t.element_size() != 1 or t.dim() != 2 or t.shape[1] < blocks:
-        raise ValueError(f"{what}: rows of at least {blocks} bytes")
-    return _tokens(what, t, dev, n, t.shape[1])
-
-
-def _call(fn, dev, *args):
-    """One launch on the current stream of device `dev`."""
-    if _torch.cuda.current_device() == dev:
-        status = fn(*args, _torch._C._cuda_getCurrentRawStream(dev))
-    else:
-        with _torch.cuda.device(dev):
-            status = fn(*args, _torch._C._cuda_getCurrentRawStream(dev))
-    if status != THL_OK:
-        raise ThlError(status, fn.__name__)
+if _torch is not None:
+    if not os.path.exists(os.path.join(_HERE, "_torch_ops.so")):
+        raise ImportError(f"{os.path.join(_HERE, '_torch_ops.so')} is not built; run __graft_entry__.build() "
+                          "or python tile_hierarchy_linear_amd/build.py")
+    from . import _torch_ops as _ops
 
 
 def rmsnorm(x, w, y, *, eps=1e-6, residual=None, residual_out=None, scale=1.0, sf=None):
     """y = the root-mean-square norm of x (+ residual) times w, in y's format; the sum goes to residual_out.
     An fp8 y holds y / scale, or MX blocks when sf takes their E8M0 scales; a uint8 y of ceil(features / 2)
     columns holds E2M1 MX blocks.  Returns y."""
-    dev = _device(x)
-    n, m = x.shape
-    px, ldx = _tokens("x", x, dev, n, m)
-    if y.dtype is _torch.uint8:
-        py, ldy = _tokens("y", y, dev, n, (m + 1) // 2)
-        types = thl_norm_types(_format(x), _NONE, _format(w), _E2M1)
-        ldy *= 2
-    else:
-        py, ldy = _tokens("y", y, dev, n, m)
-        types = thl_norm_types(_format(x), _NONE, _format(w), _format(y))
-    pw = _flat("w", w, dev, (m,))
-    pr = ldr = ps = lds = pf = ldf = 0
-    if residual is not None:
-        pr, ldr = _tokens("residual", residual, dev, n, m)
-        types.r = _format(residual)
-    if residual_out is not None:
-        if residual is None or residual_out.dtype != residual.dtype:
-            raise ValueError("residual_out: with a residual, of its type")
-        ps, lds = _tokens("residual_out", residual_out, dev, n, m)
-    if sf is not None:
-        pf, ldf = _scale_bytes("sf", sf, dev, n, (m + 31) // 32)
-    _call(_lib.thl_rmsnorm, dev, m, n, px, ldx, pr, ldr, ps, lds, pw, eps, scale, py, ldy, pf, ldf,
-          ctypes.byref(types))
+    status = _ops.rmsnorm(x, w, y, eps, residual, residual_out, scale, sf)
+    if status:
+        raise ThlError(status, "thl_rmsnorm")
     return y
 
 
 def rmsnorm_backward(s, dy, w, dx, dw=None, *, eps=1e-6, dres=None):
     """The gradients of rmsnorm for the s it normalised: dx (of x and residual alike; dres, the gradient that
     reaches s past the norm, is added) and, if wanted, dw."""
-    dev = _device(s)
-    n, m = s.shape
-    ps, lds = _tokens("s", s, dev, n, m)
-    pg, ldg = _tokens("dy", dy, dev, n, m)
-    px, ldx = _tokens("dx", dx, dev, n, m)
-    pw = _flat("w", w, dev, (m,))
-    pr = ldr = pd = pws = size = 0
-    if dres is not None:
-        pr, ldr = _tokens("dres", dres, dev, n, m)
-    if dx.dtype != dy.dtype or (dres is not None and dres.dtype != dy.dtype):
-        raise ValueError("dy, dres and dx have one type")
-    types = thl_norm_grad_types(_format(s), _format(w), _format(dy), _NONE)
-    if dw is not None:
-        pd = _flat("dw", dw, dev, (m,))
-        types.dw = _format(dw)
-        size = _lib.thl_rmsnorm_backward_workspace(m, n)
-        workspace = _torch.empty(size, dtype=_torch.uint8, device=s.device)
-        pws = workspace.data_ptr()
-    _call(_lib.thl_rmsnorm_backward, dev, m, n, ps, lds, pg, ldg, pr, ldr, pw, eps, px, ldx, pd, pws, size,
-          ctypes.byref(types))
+    status = _ops.rmsnorm_backward(s, dy, w, dx, dw, eps, dres)
+    if status:
+        raise ThlError(status, "thl_rmsnorm_backward")
 
 
 def moe_sort(ids, experts, rows, offsets, *, order=None):
     """The stable order of (tokens, choices) int32 or int64 expert ids: each choice's row (int32, -1 when its id is
     outside 0 .. experts-1), each expert's first row (experts + 1 of them), and each row's flat choice."""
-    dev = _device(ids)
-    n, topk = ids.shape
-    if ids.dtype not in (_torch.int32, _torch.int64):
-        raise ValueError("ids: int32 or int64")
-    pi, ld = _tokens("ids", ids, dev, n, topk)
-    pr = _flat("rows", rows, dev, (n, topk), _torch.int32)
-    pf = _flat("offsets", offsets, dev, (experts + 1,), _torch.int32)
-    po = _flat("order", order, dev, (n * topk,), _torch.int32) if order is not None else 0
-    size, pws = _lib.thl_moe_sort_workspace(n, topk, experts), 0
-    if size:
-        workspace = _torch.empty(size, dtype=_torch.uint8, device=ids.device)
-        pws = workspace.data_ptr()
-    _call(_lib.thl_moe_sort, dev, n, topk, experts, pi, ld, ids.element_size(), pr, pf, po, pws, size)
-
-
-def _choices(rows, dev, n):
-    """The address of (n, choices) rows, and the choices."""
-    if rows.dim() != 2:
-        raise ValueError("rows: (tokens, choices)")
-    topk = rows.shape[1]
-    return _flat("rows", rows, dev, (n, topk), _torch.int32), topk
-
-
-_PACKED = {"e2m1": 2, "i4": 2, "u4": 2, "e4m3": 1, "e5m2": 1, "i8": 1}  # elements a byte of the one-byte formats
+    status = _ops.moe_sort(ids, experts, rows, offsets, order)
+    if status:
+        raise ThlError(status, "thl_moe_sort")
 
 
 def moe_gather(x, rows, y, *, sf=None, sf_y=None, type_x=None):
     """y[rows[j, t]] = x[j], bit for bit, with the rows of block scales sf likewise into sf_y.  type_x: "e2m1" (two
     codes a byte of a uint8 tensor) where the tensor's type does not say it.  Returns y."""
-    dev = _device(x)
-    n, cols = x.shape
-    pr, topk = _choices(rows, dev, n)
-    px, ldx = _tokens("x", x, dev, n, cols)
-    rows_y = y.shape[0]
-    py, ldy = _tokens("y", y, dev, rows_y, cols)
-    if y.dtype != x.dtype:
-        raise ValueError("y has x's type")
-    packed, fmt = 1, _format(x)
-    if type_x is not None:
-        if x.element_size() != 1 or type_x not in _PACKED:
-            raise ValueError("type_x: an 8- or 4-bit format of a one-byte tensor")
-        packed, fmt = _PACKED[type_x], DTYPES[type_x]
-    m = packed * cols
-    pf = ldf = pg = ldg = 0
-    if (sf is None) != (sf_y is None):
-        raise ValueError("sf and sf_y go together")
-    if sf is not None:
-        pf, ldf = _scale_bytes("sf", sf, dev, n, (m + 31) // 32)
-        pg, ldg = _scale_bytes("sf_y", sf_y, dev, rows_y, (m + 31) // 32)
-    _call(_lib.thl_moe_gather, dev, m, n, topk, px, packed * ldx, pf, ldf, pr, rows_y, py, packed * ldy, pg, ldg, fmt)
+    status = _ops.moe_gather(x, rows, y, sf, sf_y, type_x)
+    if status:
+        raise ThlError(status, "thl_moe_gather")
     return y
 
 
 def moe_combine(x, rows, y, *, weights=None):
     """y[j] = the sum over t of weights[j, t] * x[rows[j, t]] (fp32 weights, ones without).  Returns y."""
-    dev = _device(x)
-    rows_x, m = x.shape
-    n = y.shape[0]
-    pr, topk = _choices(rows, dev, n)
-    px, ldx = _tokens("x", x, dev, rows_x, m)
-    py, ldy = _tokens("y", y, dev, n, m)
-    pw = _flat("weights", weights, dev, (n, topk), _torch.float32) if weights is not None else 0
-    _call(_lib.thl_moe_combine, dev, m, n, topk, px, ldx, rows_x, pr, pw, py, ldy, _format(x), _format(y))
+    status = _ops.moe_combine(x, rows, y, weights)
+    if status:
+        raise ThlError(status, "thl_moe_combine")
     return y
 
 
 def moe_combine_backward(dy, x, rows, weights, dx=None, dweights=None):
     """moe_combine's gradients: dx (x's type; rows that no choice has are left as they were) and dweights (fp32),
     each if wanted.  Without dweights x may be None (dx gives the rows)."""
-    dev = _device(dy)
-    like = x if x is not None else dx
-    if like is None or (dweights is not None and x is None):
-        raise ValueError("x is needed for dweights, x or dx for the rows")
-    n, m = dy.shape
-    pr, topk = _choices(rows, dev, n)
-    pg, ldg = _tokens("dy", dy, dev, n, m)
-    rows_x = like.shape[0]
-    px = ldx = pd = ldd = pw = pv = 0
-    if x is not None:
-        px, ldx = _tokens("x", x, dev, rows_x, m)
-    if dx is not None:
-        pd, ldd = _tokens("dx", dx, dev, rows_x, m)
-        if dx.dtype != like.dtype:
-            raise ValueError("dx has x's type")
-        pw = _flat("weights", weights, dev, (n, topk), _torch.float32)
-    if dweights is not None:
-        pv = _flat("dweights", dweights, dev, (n, topk), _torch.float32)
-    _call(_lib.thl_moe_combine_backward, dev, m, n, topk, pg, ldg, px, ldx, rows_x, pr, pw, pd, ldd, pv, _format(dy),
-          _format(like))
-
-
-_ACTS = {"none": 0, "relu": THL_EPI_RELU, "gelu": THL_EPI_GELU}
+    status = _ops.moe_combine_backward(dy, x, rows, weights, dx, dweights)
+    if status:
+        raise ThlError(status, "thl_moe_combine_backward")
 
 
 def gemm_w4(w, x, d, *, scales, group, type_w="u4", zeros=None, c=None, alpha=1.0, beta=0.0, bias=None, act="none"):
     """d = act(alpha * x @ W^T + beta * c + bias) for (features, K / 2) uint8 weights of two codes a byte ("u4" with
     uint8 zero points, "i4", or "e2m1" with E8M0 scales), (features, groups) scales and (tokens, K) x.  Returns d."""
-    dev = _device(x)
-    n, k = x.shape
-    m = w.shape[0]
-    if w.element_size() != 1 or type_w not in ("u4", "i4", "e2m1") or group < 1:
-        raise ValueError("w: two codes a byte, u4, i4 or e2m1, in groups of a positive length")
-    pw, ldw = _tokens("w", w, dev, m, (k + 1) // 2)
-    px, ldx = _tokens("x", x, dev, n, k)
-    pd, ldd = _tokens("d", d, dev, n, m)
-    groups = -(-k // group)
-    if type_w == "e2m1":
-        ps, lds = _scale_bytes("scales", scales, dev, m, groups)
-        ts = _E8M0
-    else:
-        ps, lds = _tokens("scales", scales, dev, m, groups)
-        ts = _format(scales)
-    pz = ldz = pc = ldc = pb = flags = 0
-    if zeros is not None:
-        pz, ldz = _scale_bytes("zeros", zeros, dev, m, groups)
-    tc = tb = _NONE
-    if beta != 0.0:
-        if c is None:
-            raise ValueError("beta without c")
-        pc, ldc = _tokens("c", c, dev, n, m)
-        tc = _format(c)
-    if bias is not None:
-        pb, tb, flags = _flat("bias", bias, dev, (m,)), _format(bias), THL_EPI_BIAS
-    gs = thl_group_scales(ps, lds, pz, ldz, group, ts)
-    dts = thl_dtypes(DTYPES[type_w], _format(x), tc, _format(d), tb, _F32)
-    epi = thl_epilogue(flags | _ACTS[act], pb, None, 0)
-    size, pws = _lib.thl_gemm_w4_workspace(n, k), 0
-    if size:
-        workspace = _torch.empty(size, dtype=_torch.uint8, device=x.device)
-        pws = workspace.data_ptr()
-    _call(_lib.thl_gemm_w4, dev, m, n, k, pw, 2 * ldw, ctypes.byref(gs), px, ldx, pc, ldc, pd, ldd, alpha, beta,
-          ctypes.byref(dts), ctypes.byref(epi), pws, size)
+    status = _ops.gemm_w4(w, x, d, scales, group, type_w, zeros, c, alpha, beta, bias, act)
+    if status:
+        raise ThlError(status, "thl_gemm_w4")
     return d
 
 

@@ -1,14 +1,18 @@
-"""Build libthl.so (HIP kernels for gfx950 + host C++) in-tree with hipcc."""
+"""Build libthl.so (HIP kernels for gfx950 + host C++) in-tree with hipcc, and
+_torch_ops.so (host C++ only) where torch is installed."""
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(os.path.dirname(HERE), "_build")
 LIB = os.path.join(HERE, "libthl.so")
+TORCH_OPS = os.path.join(HERE, "_torch_ops.so")
 PROBE_LIB = os.path.join(HERE, "libthl_probe.so")
 SOURCES = ["gemm.hip", "layout.cpp", "gemm_inst_bf16.hip", "gemm_inst_f16.hip", "gemm_inst_i8.hip",
            "gemm_inst_e4m3.hip", "gemm_inst_e2m1.hip", "gemm_inst_bf16_ops.hip", "gemm_inst_f16_ops.hip",
@@ -23,6 +27,23 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # Packed fp32 VALU instructions are switched off for every HIP compile.
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-result",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
+
+
+def build_torch_ops() -> None:
+    """The torch-tensor forms: links torch's Python and C++ libraries and libthl.so beside it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return
+    torch = list(spec.submodule_search_locations)[0]
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(HIPCC)))
+    tmp = TORCH_OPS + ".tmp"
+    subprocess.check_call(
+        [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+         "-DUSE_ROCM=1", "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(rocm, "include"),
+         "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "torch_ops.cpp"), "-o", tmp,
+         "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-L" + HERE,
+         "-l:libthl.so", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, TORCH_OPS)
 
 
 def build(verbose: bool = False) -> str:
@@ -51,6 +72,7 @@ def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
     subprocess.check_call([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC"] + objs + ["-o", tmp])
     os.replace(tmp, LIB)
+    build_torch_ops()
     # the measurement probe, a library of its own outside the GEMM boundary
     tmp = PROBE_LIB + ".tmp"
     subprocess.check_call([HIPCC] + FLAGS + ["-shared", "-x", "hip", os.path.join(CSRC, "mfma_probe.hip"), "-o", tmp],
