@@ -495,11 +495,12 @@ thl_status thl_moe_combine_backward(int64_t m, int64_t n, int64_t topk, const vo
  * a group, its zero point and scale, and the sum over groups round in fp32.
  * A token that holds an infinity or NaN gives NaN wherever integer codes meet
  * it; other tokens do not see it.  k = 0 gives act(beta*C + bias).  Any n up
- * to 2^19, but every 64 tokens stream the weights once more: this call is for
+ * to 2^21, but every 64 tokens stream the weights once more: this call is for
  * few tokens.
- *   workspace  thl_gemm_w4_workspace(n, k) bytes (0 for up to 4 tokens),
- *              16-byte aligned; not read before it is written, overlapping
- *              nothing (THL_ERR_INVALID when smaller).
+ *   workspace  thl_gemm_w4_workspace(m, n, k) bytes (0 for up to 4 tokens, and
+ *              for enough features; a few MiB otherwise), 4-byte aligned; not
+ *              read before it is written, overlapping nothing (THL_ERR_INVALID
+ *              when smaller).
  */
 typedef struct {
   const void* scales;
@@ -510,7 +511,7 @@ typedef struct {
   thl_dtype type; /* of scales */
 } thl_group_scales;
 
-size_t thl_gemm_w4_workspace(int64_t n, int64_t k);
+size_t thl_gemm_w4_workspace(int64_t m, int64_t n, int64_t k);
 thl_status thl_gemm_w4(int64_t m, int64_t n, int64_t k, const void* W, int64_t ldw, const thl_group_scales* scales,
                        const void* X, int64_t ldx, const void* C, int64_t ldc, void* D, int64_t ldd, float alpha,
                        float beta, const thl_dtypes* dtypes, const thl_epilogue* epilogue, void* workspace,

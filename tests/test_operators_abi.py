@@ -82,9 +82,10 @@ def test_workspace_sizes():
     assert thl.thl_moe_sort_workspace(512, 8, 64) == 0
     assert thl.thl_moe_sort_workspace(513, 8, 64) > 0
     assert thl.thl_moe_sort_workspace(1 << 26, 8, 64) <= 256 * 64 * 4
-    assert thl.thl_gemm_w4_workspace(4, 4096) == thl.thl_gemm_w4_workspace(40, 0) == 0
-    assert thl.thl_gemm_w4_workspace(5, 4096) == 16 * 4096 * 2
-    assert thl.thl_gemm_w4_workspace(17, 256) == 32 * 512 and thl.thl_gemm_w4_workspace(65, 257) == 128 * 1024
+    assert thl.thl_gemm_w4_workspace(4096, 4, 4096) == thl.thl_gemm_w4_workspace(4096, 40, 0) == 0
+    assert thl.thl_gemm_w4_workspace(64, 17, 256) == 0  # one pair of units: nothing to split
+    assert thl.thl_gemm_w4_workspace(64, 17, 4096) == 8 * 17 * 64 * 4
+    assert thl.thl_gemm_w4_workspace(1 << 20, 17, 4096) == 0  # enough features
     assert thl.thl_moe_sort_workspace(-1, 8, 64) == thl.thl_moe_sort_workspace(513, 8, 1 << 20) == 0
 
 
@@ -166,6 +167,7 @@ def w4(m=64, n=4, k=256, w=P[0], ldw=256, scales=P[1], ld_s=2, zeros=P[2], ld_z=
                            thl.thl_epilogue(flags, bias, None, 0), ws, size)
 
 
+LONG = dict(n=17, k=4096, ldw=4096, ldx=4096, ld_s=32, ld_z=32)  # needs a workspace
 I4 = ("i4", "bf16", "f32", "f32", "none")
 E2 = ("e2m1", "bf16", "f32", "f32", "none")
 
@@ -185,10 +187,10 @@ E2 = ("e2m1", "bf16", "f32", "f32", "none")
     (dict(types=("e4m3", "f16", "f16", "f16", "none")), UNSUPPORTED),
     (dict(types=("u4", "f32", "f16", "f16", "none")), UNSUPPORTED),
     (dict(types=("u4", "f16", "f16", "e4m3", "none")), UNSUPPORTED), (dict(acc="i32"), UNSUPPORTED),
-    (dict(m=1 << 27), UNSUPPORTED), (dict(n=1 << 20), UNSUPPORTED),
-    (dict(n=17), INVALID), (dict(n=17, ws=P[6], size=32 * 512 - 1), INVALID),
-    (dict(n=17, ws=P[6] + 8, size=1 << 20), MISALIGNED), (dict(n=17, ws=P[4], size=1 << 20), INVALID),
-    (dict(n=17, ws=P[0], size=1 << 20), INVALID), (dict(n=17, ws=P[3], size=1 << 20), INVALID),
+    (dict(m=1 << 27), UNSUPPORTED), (dict(n=1 << 22), UNSUPPORTED),
+    (dict(LONG), INVALID), (dict(LONG, ws=P[6], size=8 * 17 * 64 * 4 - 1), INVALID),
+    (dict(LONG, ws=P[6] + 2, size=1 << 20), MISALIGNED), (dict(LONG, ws=P[4], size=1 << 20), INVALID),
+    (dict(LONG, ws=P[0], size=1 << 20), INVALID), (dict(LONG, ws=P[3], size=1 << 20), INVALID),
     (dict(x=P[3] + 1), MISALIGNED), (dict(d=P[4] + 1), MISALIGNED), (dict(scales=P[1] + 1), MISALIGNED),
     (dict(d=P[0]), INVALID), (dict(d=P[1]), INVALID), (dict(d=P[2]), INVALID), (dict(d=P[3]), INVALID),
     (dict(beta=1.0, c=P[4], ldc=80), INVALID), (dict(m=0), OK), (dict(n=0), OK),

@@ -112,7 +112,7 @@ def _load():
     lib.thl_moe_combine_backward.argtypes = [i64, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp, i64, vp, i32, i32, vp]
     lib.thl_gemm_w4.argtypes = [i64, i64, i64, vp, i64, ctypes.POINTER(thl_group_scales), vp, i64, vp, i64, vp, i64,
                                 f32, f32, ctypes.POINTER(thl_dtypes), ctypes.POINTER(thl_epilogue), vp, sz, vp]
-    lib.thl_gemm_w4_workspace.argtypes = [i64, i64]
+    lib.thl_gemm_w4_workspace.argtypes = [i64, i64, i64]
     for name in ("rmsnorm", "rmsnorm_backward", "moe_sort", "moe_gather", "moe_combine", "moe_combine_backward",
                  "gemm_w4"):
         getattr(lib, "thl_" + name).restype = ctypes.c_int
@@ -360,8 +360,8 @@ def thl_moe_combine_backward(m, n, topk, DY, lddy, X, ldx, rows_x, rows, weights
                                          _dt(type_dy), _dt(type_x), stream)
 
 
-def thl_gemm_w4_workspace(n, k) -> int:
-    return _lib.thl_gemm_w4_workspace(n, k)
+def thl_gemm_w4_workspace(m, n, k) -> int:
+    return _lib.thl_gemm_w4_workspace(m, n, k)
 
 
 def thl_gemm_w4(m, n, k, W, ldw, scales, X, ldx, C, ldc, D, ldd, alpha, beta, dtypes, epilogue=None, workspace=None,

@@ -376,7 +376,7 @@ thl_status gemm_w4(PyObject* const* a) {
     dt.bias = static_cast<thl_dtype>(format("bias", b));
   }
   Launch l(dev);
-  const size_t need = thl_gemm_w4_workspace(n, k);
+  const size_t need = thl_gemm_w4_workspace(m, n, k);
   void* ws = l.take(need);
   return thl_gemm_w4(m, n, k, mw.p, 2 * mw.ld, &gs, mx.p, mx.ld, mc.p, mc.ld, md.p, md.ld, alpha, beta, &dt, &epi, ws,
                      need, l.stream);

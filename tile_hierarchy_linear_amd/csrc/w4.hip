@@ -38,7 +38,7 @@ struct W4Args {
   const void* scales;
   const uint8_t* zeros;  // unsigned codes only
   const uint16_t* x;
-  uint8_t* packed;       // more than 16 tokens: X in operand order
+  float* sums;           // K split over workgroups: the splits' n x m sums
   const void* c;
   void* d;
   const void* bias;
@@ -49,6 +49,8 @@ struct W4Args {
   int32_t c_type, d_type, bias_type, flags;
   float alpha, beta;
 };
+
+constexpr int64_t kMaxTokens = INT64_C(1) << 21;  // workgroups of 64 in a grid's rows
 
 enum : int { W_U4 = 0, W_I4 = 1, W_E2M1 = 2 };
 
@@ -309,20 +311,6 @@ __device__ __forceinline__ void store_result(const W4Args& a, float v, int64_t i
     static_cast<__bf16*>(a.d)[at] = static_cast<__bf16>(v);
 }
 
-// Sums of TILE = tiles * 256 values over the wavefronts, in wavefront order,
-// and the epilogue.  Value q of `part` is register r, lane l of tile (b, t).
-template <int MT, int NB>
-__device__ __forceinline__ void finish(const W4Args& a, const float* part, int waves, int i0, int j0) {
-  constexpr int TILE = NB * MT * 256;
-  for (int q = static_cast<int>(threadIdx.x); q < TILE; q += static_cast<int>(blockDim.x)) {
-    const int l = q & 63, r = (q >> 6) & 3, t = (q >> 8) % MT, b = (q >> 8) / MT;
-    const int i = i0 + 16 * b + (l & 15), j = j0 + 16 * t + 4 * r + (l >> 4);
-    float v = part[q];
-    for (int s = 1; s < waves; ++s) v += part[s * TILE + q];
-    store_result(a, v, i, j);
-  }
-}
-
 // ---- up to four tokens
 // No matrix cores: a lane takes 32 consecutive codes of a row, the lanes of a
 // wavefront a run of 2,048 codes (1 KB), so that loads are whole lines in lane
@@ -528,55 +516,59 @@ __global__ void __launch_bounds__(kOneWaves * 64) w4_one_kernel(W4Args a, int ks
 }
 
 // ---- more tokens
-// A wavefront takes 32 features and all of the workgroup's 16 MT tokens over
-// its share of K: a weight is decoded once for all of them, an activation
-// fragment serves both feature tiles.  Every wavefront reads every
-// activation of its units, from L2: read where they lie, 16 rows of 64 bytes
-// an instruction, they would set the pace (8192 x 48 x 8192 on E2M1: 33 us).
-// So a first kernel writes them in operand order, a fragment's 64 lanes side
-// by side, padded with zeros to whole units and tiles.
+// On the matrix cores.  A workgroup takes 128 features, its wavefronts four
+// groups of 32 times KW units of K; a weight is decoded once for all of the
+// workgroup's 16 MT tokens, and the activations of KW units go through LDS
+// once for all features, in operand order, the next ones on their way in
+// registers.  KW is 1 with one token tile, where a CU holds several small
+// workgroups whose barriers do not meet (8192 x 16 x 8192, signed codes, groups
+// of 128: 16.8 against 19.5 us), and 2 with more (28672 x 64 x 8192: 67.6
+// against 71.3 us).  (Read by each wavefront for itself they set the pace: 8192 x
+// 48 x 8192 moved 200 MB of activations from L2 and took 21 us.)  Where the
+// features alone leave compute units idle, K is split over workgroups too;
+// the splits' sums then go to the workspace and a second kernel adds them in
+// order.
+//
+// Codes are loaded along the rows, eight lanes a row's 128 bytes of a unit,
+// and turned into operand order through LDS (in operand order neighbouring
+// lanes hold different rows, and a load takes a cache access a lane instead of
+// one for four).
+constexpr int kManyFeatures = 128;
 
-// Fragment (tile, unit, step): 64 pieces of eight activations, lane l's at
-// 16 l bytes, for row l % 16 of the tile and lane group l / 16.
-__device__ __forceinline__ int64_t fragment(int64_t tile, int64_t units, int64_t u, int step) {
-  return ((tile * units + u) * 8 + step) * 64;
+// What the row of an activation piece is turned by in LDS, by the two-bit
+// halves of its place along K: sixteen values, and between the lane groups
+// that read together none that maps their rows onto one another.
+__device__ __forceinline__ int swizzle(int high, int low) {
+  return ((high & 1) << 3) | (((high ^ (high >> 1)) & 1) << 2) | low;
 }
 
-// One workgroup per unit and tile: 16 tokens x 256 K.
-template <int WT>
-__global__ void __launch_bounds__(256) w4_pack_kernel(W4Args a, int turned) {
-  const int64_t u = blockIdx.x, tile = blockIdx.y, units = gridDim.x;
-  v4i* out = reinterpret_cast<v4i*>(a.packed);
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int p = static_cast<int>(threadIdx.x) + 256 * q, kp = p & 31, row = p >> 5;
-    const int64_t k0 = 256 * u + 8 * kp, j = 16 * tile + 4 * (row & 3) + (row >> 2);
-    v4i x = {0, 0, 0, 0};
-    if (j < a.n && k0 < a.k) x = load_x8(a.x + j * a.ldx + k0, a.k - k0 < 8 ? static_cast<int>(a.k - k0) : 8);
-    const int h = kp >> 4, hi = (kp >> 2) & 3, lo = kp & 3;
-    out[fragment(tile, units, u, 4 * h + (turned ? hi : lo)) + 16 * (turned ? lo : hi) + row] = in_order<WT>(x);
-  }
-}
+constexpr int units_at_once(int mt) { return mt == 1 ? 1 : 2; }
 
-template <int WT, bool BF, int GPU, int MT, int NB>
-__global__ void __launch_bounds__(512) w4_many_kernel(W4Args a) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t area[];  // the codes of a unit by wavefront, then the sums
-  constexpr int LEN = 256 / GPU;
+template <int WT, bool BF, int GPU, int MT>
+__global__ void __launch_bounds__(256 * units_at_once(MT)) w4_many_kernel(W4Args a) {
+  constexpr int NB = 2, FW = 4, KW = units_at_once(MT);
+  constexpr int PASSES = 2 / KW;  // to move sixteen rows of 32 pieces
+  constexpr int LEN = 256 / GPU;  // codes per group within a unit
   constexpr bool TURN = LEN < 128, FOLD = WT == W_E2M1 && BF;
-  constexpr int RING = MT == 4 && !FOLD ? 4 : 8;  // steps of activations on their way (registers allow)
-  const int lane = static_cast<int>(threadIdx.x) & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
-  const int waves = static_cast<int>(blockDim.x) >> 6;
+  // Activations: [buffer][unit][tile][step][lane group][row],
+  // eight a piece; piece kp of a row's unit lies at row ^ swizzle, so that neither
+  // the writes (along kp) nor the reads (along the rows) meet in a bank.
+  __shared__ __attribute__((aligned(16))) v4i xbuf[2][KW * MT * 512];
+  // Codes of a wavefront's unit: position p of row r holds its 16-byte chunk p ^ (r % 8).
+  __shared__ __attribute__((aligned(16))) v4i turned[FW * KW][NB * 128];
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int fw = wave % FW, kw = wave / FW;
   const int col = lane & 15, g = lane >> 4;
-  const int i0 = static_cast<int>(blockIdx.x) * 16 * NB, j0 = static_cast<int>(blockIdx.y) * 16 * MT;
+  const int i0 = static_cast<int>(blockIdx.x) * kManyFeatures + 32 * fw, j0 = static_cast<int>(blockIdx.y) * 16 * MT;
+  const int split = static_cast<int>(blockIdx.z), splits = static_cast<int>(gridDim.z);
   const int units = static_cast<int>((static_cast<int64_t>(a.k) + 255) >> 8), whole = a.k >> 8;
+  const int sets = (whole + KW - 1) / KW;  // of KW units
+  const int beg = static_cast<int>(static_cast<int64_t>(split) * sets / splits);
+  const int len = static_cast<int>(static_cast<int64_t>(split + 1) * sets / splits) - beg;
 
-  // Codes are loaded along the rows, eight lanes a row's 128 bytes of a unit,
-  // and turned into operand order through LDS (in operand order neighbouring
-  // lanes hold different rows, and a load takes a cache access a lane instead
-  // of one for four).  Position p of row r holds its 16-byte chunk p ^ (r % 8),
-  // so that neither the writes nor the reads meet in a bank.
-  // Features past m repeat the last one; nothing of them is stored.
+  // Features past m and tokens past n repeat the last one; nothing of them
+  // is stored.
   auto feature = [&](int i) { return static_cast<int64_t>(i < a.m ? i : a.m - 1); };
   const uint8_t* w[NB][2];
 #pragma unroll
@@ -584,72 +576,132 @@ __global__ void __launch_bounds__(512) w4_many_kernel(W4Args a) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       w[b][h] = a.w + feature(i0 + 16 * b + 8 * h + (lane >> 3)) * a.ldw_bytes + 16 * (lane & 7);
-  v4i* const turned = reinterpret_cast<v4i*>(area) + wave * NB * 128;
   const int put = (lane >> 3) * 8 + ((lane & 7) ^ (lane >> 3));  // row lane / 8 of the first eight
   const int get = col * 8 + (g ^ (col & 7));                     // chunk g of row col (chunk 4 + g: ^ 4)
-  // Scales: lane group g asks for tile g % NB of the unit g / NB turns on,
-  // 4 / NB units at a time.
+  // Scales: lane group g asks for tile g % NB of its wavefront's unit g / NB
+  // sets on, 4 / NB units at a time.
   constexpr int UNITS = 4 / NB;
   const int64_t gi = feature(i0 + 16 * (g % NB) + col);
   const int64_t srow = gi * a.ld_scales, zrow = gi * a.ld_zeros;
-  const v4i* x = reinterpret_cast<const v4i*>(a.packed) + fragment(blockIdx.y * MT, units, 0, 0) + lane;
 
+  // Unit k2 of this workgroup's q-th set.  Every load of the loop is issued
+  // whatever the position, of a unit that exists: with loads behind branches
+  // the compiler waits for all of them at each use.
+  auto unit_of = [&](int q, int k2) {
+    const int u = KW * (beg + (q < len ? q : len - 1)) + k2;
+    return u < whole ? u : whole - 1;
+  };
   v4i ring[2][NB][2];
-  // Every load is issued whatever the position, of a unit that exists: with
-  // loads behind branches the compiler waits for all of them at each use.
-  auto load = [&](int v, v4i (&o)[NB][2]) {
-    const int64_t u = v < whole ? v : whole - 1;
+  auto load = [&](int q, v4i (&o)[NB][2]) {
+    const int64_t u = unit_of(q, kw);
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         o[b][h] = __builtin_nontemporal_load(reinterpret_cast<const v4i_a1*>(w[b][h] + 128 * u));
   };
-  auto load_scales = [&](int v, Groups<WT, GPU>& o) {
-    const int u = v + waves * (g / NB);
-    load_groups<WT, GPU>(a, srow, zrow, u < whole ? u : whole - 1, o);
+  auto load_scales = [&](int q, Groups<WT, GPU>& o) {
+    load_groups<WT, GPU>(a, srow, zrow, unit_of(q + g / NB, kw), o);
   };
-  // Fragments of step s (0 .. 7) of unit u.
-  v4i xa[RING][MT];
-  auto fetch = [&](int v, int s, v4i (&o)[MT]) {
-    const int u = v < units ? v : units - 1;
+
+  // A lane moves piece kp of row `row` (and row + 8, in two passes) of every
+  // unit and tile.  Row r of a
+  // token tile is token 4 (r % 4) + r / 4, so that register r of lane group g
+  // of the sums is token 4 r + g.
+  const int kp = tid & 31, row = tid >> 5;
+  auto place_at = [&](int r) {
+    return ((kp >> 4) * 4 + (TURN ? (kp >> 2) & 3 : kp & 3)) * 64 + (TURN ? kp & 3 : (kp >> 2) & 3) * 16 +
+           (r ^ swizzle(kp >> 2 & 3, kp & 3));
+  };
+  const uint16_t* x[MT][PASSES];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) o[t] = x[fragment(t, units, u, s)];
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int h = 0; h < PASSES; ++h) {
+      const int r = row + 8 * h, j = j0 + 16 * t + 4 * (r & 3) + (r >> 2);
+      x[t][h] = a.x + static_cast<int64_t>(j < a.n ? j : a.n - 1) * a.ldx + 8 * kp;
+    }
+  v4i pre[KW][MT][PASSES];
+  auto fetch = [&](int q) {
+#pragma unroll
+    for (int k2 = 0; k2 < KW; ++k2) {
+      const int64_t u = unit_of(q, k2);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int h = 0; h < PASSES; ++h) pre[k2][t][h] = *reinterpret_cast<const v4i_a2*>(x[t][h] + 256 * u);
+    }
+  };
+  auto place = [&](int buffer) {
+#pragma unroll
+    for (int k2 = 0; k2 < KW; ++k2)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int h = 0; h < PASSES; ++h)
+          xbuf[buffer][(k2 * MT + t) * 512 + place_at(row + 8 * h)] = in_order<WT>(pre[k2][t][h]);
   };
 
   v4f tot[NB][MT] = {}, acc[NB][MT] = {}, xs[MT] = {};
-  // Unit u of this wavefront, its codes in operand order.
-  auto use = [&](int u, const v4i (&codes)[NB][2], const Groups<WT, GPU> (&groups)[NB]) {
+  // One unit: its codes in operand order, its activations as unit k2 of a buffer.
+  auto use = [&](int buffer, int k2, const v4i (&codes)[NB][2], const Groups<WT, GPU> (&groups)[NB]) {
+    v4i wq[NB][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) wq[b][h] = TURN ? turn(codes[b][h]) : codes[b][h];
+    const v4i* from = &xbuf[buffer][k2 * MT * 512 + g * 16];
+    auto read = [&](int s8, v4i (&o)[MT]) {
+      const int at = s8 * 64 + (col ^ (TURN ? swizzle(s8 & 3, g) : swizzle(g, s8 & 3)));
+#pragma unroll
+      for (int t = 0; t < MT; ++t) o[t] = from[t * 512 + at];
+    };
+    // Step s8's weights as 16-bit floats.
+    auto weights = [&](int s8, v4i (&o)[NB]) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        o[b] = decode<WT, BF>(static_cast<uint32_t>(wq[b][s8 >> 2][s8 & 3]),
+                              FOLD ? group_scale<WT, GPU>(a, groups[b], s8) : 1.0f);
+    };
+    v4i xa[2][MT], wf[2][NB];
+    read(0, xa[0]);
+    weights(0, wf[0]);
 #pragma unroll
     for (int s8 = 0; s8 < 8; ++s8) {
       const int h = s8 >> 2, s = s8 & 3;
-      // one step's operands at a time: mixing the steps costs more registers
-      // than there are
+      // One step's products at a time (mixing the steps costs more registers
+      // than there are), with the next step's operands made in their shadow.
       __builtin_amdgcn_sched_barrier(0);
-      v4i (&xf)[MT] = xa[s8 % RING];
+      if (s8 < 7) {
+        read(s8 + 1, xa[(s8 + 1) & 1]);
+        weights(s8 + 1, wf[(s8 + 1) & 1]);
+      }
+      const v4i (&xf)[MT] = xa[s8 & 1];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const v4i wq = TURN ? turn(codes[b][h]) : codes[b][h];
-        const uint32_t c = static_cast<uint32_t>(wq[s]);
-        const v4i wf = decode<WT, BF>(c, FOLD ? group_scale<WT, GPU>(a, groups[b], s8) : 1.0f);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           if constexpr (FOLD)
-            tot[b][t] = mfma16<BF>(xf[t], wf, tot[b][t]);
+            tot[b][t] = mfma16<BF>(xf[t], wf[s8 & 1][b], tot[b][t]);
           else
-            acc[b][t] = mfma16<BF>(xf[t], wf, acc[b][t]);
+            acc[b][t] = mfma16<BF>(xf[t], wf[s8 & 1][b], acc[b][t]);
         }
       }
       if constexpr (is_int(WT)) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) xs[t] = mfma16<BF>(xf[t], ones<BF>(), xs[t]);
       }
-      // this step's slot takes the activations RING steps on
-      fetch(s8 + RING < 8 ? u : u + waves, (s8 + RING) & 7, xf);
+#pragma unroll
+      for (int i = 0; i < (NB + (is_int(WT) ? 1 : 0)) * MT; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // a read of LDS
+        __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);  // three vector instructions
+      }
       const int done = 32 * (s8 + 1);
       if (FOLD) {
         // the scales are in the products
       } else if (TURN ? done % LEN == 0 : (s == 3 && (LEN == 128 || h == 1))) {
+        __builtin_amdgcn_sched_barrier(0);
         const int q = (done - 1) / LEN;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -666,94 +718,141 @@ __global__ void __launch_bounds__(512) w4_many_kernel(W4Args a) {
       }
     }
   };
-
-  auto turn_and_use = [&](int u, const v4i (&in)[NB][2], const Groups<WT, GPU> (&groups)[NB]) {
+  auto turn_and_use = [&](int buffer, const v4i (&in)[NB][2], const Groups<WT, GPU> (&groups)[NB]) {
     v4i codes[NB][2];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) turned[b * 128 + h * 64 + put] = in[b][h];
+      for (int h = 0; h < 2; ++h) turned[wave][b * 128 + h * 64 + put] = in[b][h];
     __builtin_amdgcn_wave_barrier();  // a wavefront's LDS accesses run in order
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) codes[b][h] = turned[b * 128 + (get ^ (4 * h))];
+      for (int h = 0; h < 2; ++h) codes[b][h] = turned[wave][b * 128 + (get ^ (4 * h))];
     __builtin_amdgcn_wave_barrier();
-    use(u, codes, groups);
+    use(buffer, kw, codes, groups);
   };
 
-  // The wavefronts take the units in turn.  Loads return in order, so a
-  // unit's weights are asked for after the activations of the unit before:
-  // those then do not wait for memory.
-  if (wave < whole) {
+  if (len > 0) {
     Groups<WT, GPU> asked;
-    load_scales(wave, asked);
-    load(wave, ring[0]);
-#pragma unroll
-    for (int s = 0; s < RING; ++s) fetch(wave, s, xa[s]);
-    load(wave + waves, ring[1]);
-    bool more = true;
-    for (int u = wave; more;) {
+    load_scales(0, asked);
+    load(0, ring[0]);
+    fetch(0);
+    place(0);
+    fetch(1);
+    load(1, ring[1]);
+    for (int q = 0; q < len;) {
       // the scales of the next UNITS units, one set of tiles a unit
       constexpr int SW = sizeof(asked.s) / 4, ZW = sizeof(asked.z) / 4;
       Groups<WT, GPU> groups[4];
 #pragma unroll
-      for (int q = 0; q < SW; ++q) {
+      for (int i = 0; i < SW; ++i) {
         uint32_t o[4];
-        spread(asked.s[q], o);
+        spread(asked.s[i], o);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) groups[j].s[q] = o[j];
+        for (int j = 0; j < 4; ++j) groups[j].s[i] = o[j];
       }
       if constexpr (WT == W_U4) {
 #pragma unroll
-        for (int q = 0; q < ZW; ++q) {
+        for (int i = 0; i < ZW; ++i) {
           uint32_t o[4];
-          spread(asked.z[q], o);
+          spread(asked.z[i], o);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) groups[j].z[q] = o[j];
+          for (int j = 0; j < 4; ++j) groups[j].z[i] = o[j];
         }
       }
-      load_scales(u + UNITS * waves, asked);
+      load_scales(q + UNITS, asked);
 #pragma unroll
       for (int d = 0; d < UNITS; ++d) {
+        if (q >= len) break;
+        // buffer d is whole, and nobody reads the other one any more
+        __syncthreads();
+        place(d ^ 1);
+        fetch(q + 2);
         Groups<WT, GPU> mine[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) mine[b] = groups[d * NB + b];
-        turn_and_use(u, ring[d & 1], mine);
-        load(u + 2 * waves, ring[d & 1]);
-        u += waves;
-        if (u >= whole) {
-          more = false;
-          break;
-        }
+        if (KW == 1 || KW * (beg + q) + kw < whole) turn_and_use(d, ring[d], mine);
+        load(q + 2, ring[d]);
+        ++q;
       }
     }
   }
-  if (whole < units && wave == whole % waves) {  // K's partial unit
-    v4i codes[NB][2];
-    Groups<WT, GPU> groups[NB];
+  if (whole < units && split == splits - 1) {  // K's partial unit
+    __syncthreads();
+    const int64_t left = a.k - (256 * static_cast<int64_t>(whole) + 8 * kp);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int64_t i = feature(i0 + 16 * b + col);
-      load_codes_end(a, a.w + i * a.ldw_bytes, whole, g, codes[b]);
-      load_groups_end<WT, GPU>(a, i * a.ld_scales, i * a.ld_zeros, whole, groups[b]);
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int h = 0; h < PASSES; ++h)
+        xbuf[0][t * 512 + place_at(row + 8 * h)] = in_order<WT>(
+            load_x8(x[t][h] + 256 * static_cast<int64_t>(whole), left < 8 ? static_cast<int>(left < 0 ? 0 : left) : 8));
+    __syncthreads();
+    if (kw == 0) {
+      v4i codes[NB][2];
+      Groups<WT, GPU> groups[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int64_t i = feature(i0 + 16 * b + col);
+        load_codes_end(a, a.w + i * a.ldw_bytes, whole, g, codes[b]);
+        load_groups_end<WT, GPU>(a, i * a.ld_scales, i * a.ld_zeros, whole, groups[b]);
+      }
+      use(0, 0, codes, groups);
     }
-#pragma unroll
-    for (int s = 0; s < RING; ++s) fetch(whole, s, xa[s]);
-    use(whole, codes, groups);
   }
 
-  float* const part = reinterpret_cast<float*>(area);  // [wavefront][NB][MT][4][64]
-  __syncthreads();
-  constexpr int TILE = NB * MT * 256;
+  if constexpr (KW == 2) {
+    // The two units' sums, the first's first.
+    float* const part = reinterpret_cast<float*>(&xbuf[0][0]) + fw * NB * MT * 256 + lane;
+    static_assert(sizeof(xbuf) >= FW * NB * MT * 1024, "the sums fit the activations' area");
+    __syncthreads();
+    if (kw == 1) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) part[((b * MT + t) * 4 + r) * 64] = tot[b][t][r];
+    }
+    __syncthreads();
+    if (kw != 0) return;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) tot[b][t][r] += part[((b * MT + t) * 4 + r) * 64];
+  }
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) part[wave * TILE + ((b * MT + t) * 4 + r) * 64 + lane] = tot[b][t][r];
-  __syncthreads();
-  finish<MT, NB>(a, part, waves, i0, j0);
+      for (int r = 0; r < 4; ++r) {
+        const int64_t i = i0 + 16 * b + col, j = j0 + 16 * t + 4 * r + g;
+        if (splits == 1)
+          store_result(a, tot[b][t][r], i, j);
+        else if (i < a.m && j < a.n)
+          a.sums[(static_cast<int64_t>(split) * a.n + j) * a.m + i] = tot[b][t][r];
+      }
+}
+
+// The splits' sums, in order, and the epilogue.
+__global__ void __launch_bounds__(256) w4_splits_kernel(W4Args a, int splits) {
+  const int64_t total = static_cast<int64_t>(a.n) * a.m;
+  for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < total;
+       q += static_cast<int64_t>(gridDim.x) * 256) {
+    float v = 0.0f;
+    for (int s = 0; s < splits; s += 4) {
+      float t[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] = a.sums[(s + i < splits ? s + i : s) * total + q];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v += s + i < splits ? t[i] : 0.0f;
+    }
+    const int64_t j = q / a.m;
+    store_result(a, v, q - j * a.m, j);
+  }
 }
 
 template <int WT, bool BF, int NT>
@@ -772,44 +871,40 @@ hipError_t launch_one(W4Args& a, hipStream_t st) {
                          dim3(kOneWaves * 64), args, 0, st);
 }
 
-// Tokens padded to whole tiles of the kernel that takes them.
-int64_t padded_tokens(int64_t n) {
-  const int64_t tile = n <= 16 ? 16 : (n <= 32 ? 32 : (n <= 48 ? 48 : 64));
-  return (n + tile - 1) / tile * tile;
+// Token tiles of sixteen per workgroup, and workgroups along the tokens.
+int tiles_for(int64_t n) { return n <= 16 ? 1 : (n <= 32 ? 2 : (n <= 48 ? 3 : 4)); }
+
+// Ways to split K over workgroups: as many as bring their number to one a CU
+// (two with one token tile), of at least two units of K each.
+int64_t splits_of(int64_t m, int64_t n, int64_t k) {
+  const int mt = tiles_for(n);
+  const int64_t blocks = (m + kManyFeatures - 1) / kManyFeatures * ((n + 16 * mt - 1) / (16 * mt));
+  const int64_t most = k / 512, want = (mt == 1 ? 512 : 256) / blocks;
+  const int64_t s = want < most ? want : most;
+  return s > 1 ? s : 1;
 }
 
-template <int WT, bool BF, int GPU, int MT, int NB>
-hipError_t launch_many(W4Args& a, hipStream_t st) {
-  const int64_t units = (static_cast<int64_t>(a.k) + 255) / 256, gy = padded_tokens(a.n) / (16 * MT);
-  if (units > 0) {
-    int turned = 256 / GPU < 128;
-    void* args[] = {&a, &turned};
-    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(&w4_pack_kernel<WT>),
-                                         dim3(static_cast<unsigned>(units), static_cast<unsigned>(gy * MT)), dim3(256),
-                                         args, 0, st);
-    if (e != hipSuccess) return e;
-  }
-  int waves = 8;
-  while (waves > 1 && waves > units) waves /= 2;
-  void* args[] = {&a};
-  return hipLaunchKernel(reinterpret_cast<const void*>(&w4_many_kernel<WT, BF, GPU, MT, NB>),
-                         dim3(static_cast<unsigned>((a.m + 16 * NB - 1) / (16 * NB)), static_cast<unsigned>(gy)), dim3(waves * 64), args,
-                         static_cast<size_t>(waves) * NB * (MT > 2 ? MT : 2) * 1024, st);
-}
-
-// Two feature tiles a wavefront read each activation once for both; one
-// where two would leave compute units without a workgroup.
 template <int WT, bool BF, int GPU, int MT>
 hipError_t launch_many(W4Args& a, hipStream_t st) {
-  return a.m <= 4096 ? launch_many<WT, BF, GPU, MT, 1>(a, st) : launch_many<WT, BF, GPU, MT, 2>(a, st);
+  int splits = static_cast<int>(splits_of(a.m, a.n, a.k));
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.m) + kManyFeatures - 1) / kManyFeatures),
+                  static_cast<unsigned>((static_cast<int64_t>(a.n) + 16 * MT - 1) / (16 * MT)),
+                  static_cast<unsigned>(splits));
+  void* args[] = {&a, &splits};
+  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(&w4_many_kernel<WT, BF, GPU, MT>), grid,
+                                       dim3(256 * units_at_once(MT)), args, 0, st);
+  if (e != hipSuccess || splits == 1) return e;
+  const int64_t blocks = (static_cast<int64_t>(a.n) * a.m + 255) / 256;
+  return hipLaunchKernel(reinterpret_cast<const void*>(&w4_splits_kernel),
+                         dim3(static_cast<unsigned>(blocks < 8192 ? blocks : 8192)), dim3(256), args, 0, st);
 }
 
 template <int WT, bool BF, int GPU>
 hipError_t launch_tokens(W4Args& a, hipStream_t st) {
   if (a.n <= 16) return launch_many<WT, BF, GPU, 1>(a, st);
   if (a.n <= 32) return launch_many<WT, BF, GPU, 2>(a, st);
-  if (a.n <= 48) return launch_many<WT, BF, GPU, 3, 2>(a, st);
-  return launch_many<WT, BF, GPU, 4, 2>(a, st);
+  if (a.n <= 48) return launch_many<WT, BF, GPU, 3>(a, st);
+  return launch_many<WT, BF, GPU, 4>(a, st);
 }
 
 template <int WT, bool BF>
@@ -839,7 +934,7 @@ hipError_t launch_type(W4Args& a, thl_dtype w, hipStream_t st) {
   return w == THL_U4X2 ? launch_weights<W_U4, BF>(a, st) : launch_weights<W_I4, BF>(a, st);
 }
 
-constexpr int64_t kMaxTokens = INT64_C(1) << 19;  // tiles of 16 in a grid's rows
+
 
 bool big(int64_t v) { return v > INT32_MAX; }
 int64_t at_least_one(int64_t v) { return v > 1 ? v : 1; }
@@ -852,9 +947,10 @@ using namespace thl;
 
 extern "C" {
 
-size_t thl_gemm_w4_workspace(int64_t n, int64_t k) {
-  if (n <= 4 || n > kMaxTokens || k <= 0 || big(k)) return 0;
-  return static_cast<size_t>(padded_tokens(n)) * static_cast<size_t>((k + 255) / 256) * 512;
+size_t thl_gemm_w4_workspace(int64_t m, int64_t n, int64_t k) {
+  if (m <= 0 || m > kMaxFeatures || n <= 4 || n > kMaxTokens || k <= 0 || big(k)) return 0;
+  const int64_t s = splits_of(m, n, k);
+  return s == 1 ? 0 : static_cast<size_t>(s) * static_cast<size_t>(n) * static_cast<size_t>(m) * sizeof(float);
 }
 
 thl_status thl_gemm_w4(int64_t m, int64_t n, int64_t k, const void* W, int64_t ldw,
@@ -904,9 +1000,9 @@ thl_status thl_gemm_w4(int64_t m, int64_t n, int64_t k, const void* W, int64_t l
       (has_bias && misaligned(bias, dt->bias)) || misaligned(gs->scales, gs->type))
     return THL_ERR_MISALIGNED;
 
-  const size_t need = thl_gemm_w4_workspace(n, k);
+  const size_t need = thl_gemm_w4_workspace(m, n, k);
   if (need && (!workspace || workspace_bytes < need)) return THL_ERR_INVALID;
-  if (need && reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return THL_ERR_MISALIGNED;
+  if (need && reinterpret_cast<uintptr_t>(workspace) % 4 != 0) return THL_ERR_MISALIGNED;
 
   // ---- overlap: D may alias C exactly; the workspace overlaps nothing
   const Range rd = matrix_range(D, dt->d, m, n, ldd);
@@ -930,7 +1026,7 @@ thl_status thl_gemm_w4(int64_t m, int64_t n, int64_t k, const void* W, int64_t l
 
   W4Args a{};
   a.w = static_cast<const uint8_t*>(W), a.scales = gs->scales, a.zeros = u4 ? gs->zeros : nullptr;
-  a.x = static_cast<const uint16_t*>(X), a.packed = static_cast<uint8_t*>(workspace), a.c = C, a.d = D, a.bias = bias;
+  a.x = static_cast<const uint16_t*>(X), a.sums = static_cast<float*>(workspace), a.c = C, a.d = D, a.bias = bias;
   a.ldw_bytes = ldw / 2, a.ld_scales = gs->ld_scales, a.ld_zeros = u4 ? gs->ld_zeros : 0;
   a.ldx = ldx, a.ldc = ldc, a.ldd = ldd;
   a.m = static_cast<int32_t>(m), a.n = static_cast<int32_t>(n), a.k = static_cast<int32_t>(k);
