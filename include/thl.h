@@ -497,7 +497,7 @@ thl_status thl_moe_combine_backward(int64_t m, int64_t n, int64_t topk, const vo
  * it; other tokens do not see it.  k = 0 gives act(beta*C + bias).  Any n up
  * to 2^21, but every 64 tokens stream the weights once more: this call is for
  * few tokens.
- *   workspace  thl_gemm_w4_workspace(m, n, k) bytes (0 for up to 4 tokens, and
+ *   workspace  thl_gemm_w4_workspace(m, n, k) bytes (0 for one or two tokens, and
  *              for enough features; a few MiB otherwise), 4-byte aligned; not
  *              read before it is written, overlapping nothing (THL_ERR_INVALID
  *              when smaller).

@@ -82,7 +82,7 @@ def test_workspace_sizes():
     assert thl.thl_moe_sort_workspace(512, 8, 64) == 0
     assert thl.thl_moe_sort_workspace(513, 8, 64) > 0
     assert thl.thl_moe_sort_workspace(1 << 26, 8, 64) <= 256 * 64 * 4
-    assert thl.thl_gemm_w4_workspace(4096, 4, 4096) == thl.thl_gemm_w4_workspace(4096, 40, 0) == 0
+    assert thl.thl_gemm_w4_workspace(4096, 2, 4096) == thl.thl_gemm_w4_workspace(4096, 40, 0) == 0
     assert thl.thl_gemm_w4_workspace(64, 17, 256) == 0  # one pair of units: nothing to split
     assert thl.thl_gemm_w4_workspace(64, 17, 4096) == 8 * 17 * 64 * 4
     assert thl.thl_gemm_w4_workspace(1 << 20, 17, 4096) == 0  # enough features

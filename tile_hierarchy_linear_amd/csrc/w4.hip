@@ -311,7 +311,7 @@ __device__ __forceinline__ void store_result(const W4Args& a, float v, int64_t i
     static_cast<__bf16*>(a.d)[at] = static_cast<__bf16>(v);
 }
 
-// ---- up to four tokens
+// ---- one or two tokens
 // No matrix cores: a lane takes 32 consecutive codes of a row, the lanes of a
 // wavefront a run of 2,048 codes (1 KB), so that loads are whole lines in lane
 // order, and its 32 activations a token stay in registers while the wavefront
@@ -907,11 +907,14 @@ hipError_t launch_tokens(W4Args& a, hipStream_t st) {
   return launch_many<WT, BF, GPU, 4>(a, st);
 }
 
+// One and two tokens go down the rows, more to the matrix cores: with four
+// tokens' activations in registers a CU holds half the wavefronts (8192 x 4 x
+// 8192, unsigned codes, groups of 128: 21.2 us down the rows, 15.5 on the
+// matrix cores; two tokens, 28672 x 2 x 8192: 30 against 36 us).
 template <int WT, bool BF>
 hipError_t launch_weights(W4Args& a, hipStream_t st) {
   if (a.n == 1) return launch_one<WT, BF, 1>(a, st);
   if (a.n == 2) return launch_one<WT, BF, 2>(a, st);
-  if (a.n <= 4) return launch_one<WT, BF, 4>(a, st);
   if constexpr (WT == W_E2M1) {
     return launch_tokens<WT, BF, 8>(a, st);
   } else {
@@ -948,7 +951,7 @@ using namespace thl;
 extern "C" {
 
 size_t thl_gemm_w4_workspace(int64_t m, int64_t n, int64_t k) {
-  if (m <= 0 || m > kMaxFeatures || n <= 4 || n > kMaxTokens || k <= 0 || big(k)) return 0;
+  if (m <= 0 || m > kMaxFeatures || n <= 2 || n > kMaxTokens || k <= 0 || big(k)) return 0;
   const int64_t s = splits_of(m, n, k);
   return s == 1 ? 0 : static_cast<size_t>(s) * static_cast<size_t>(n) * static_cast<size_t>(m) * sizeof(float);
 }
