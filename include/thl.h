@@ -454,7 +454,7 @@ thl_status thl_moe_gather(int64_t m, int64_t n, int64_t topk, const void* X, int
 /*
  * thl_moe_combine -- Y(:, j) = sum over t of weights[j*topk + t] * X(:,
  * rows[j*topk + t]), in fp32 in the order of t, rounded once.  Choices without
- * a place in 0 .. rows_x-1 add nothing (and their weight is not read); a token
+ * a place in 0 .. rows_x-1 add nothing, whatever their weight; a token
  * without any gets zeros.  weights = NULL: ones.  F32, F16 or BF16 for X and
  * for Y.  Y may not overlap another array.
  */
