@@ -224,16 +224,30 @@ struct GatherArgs {
   int32_t topk, lanes;          // lanes per token, a power of two up to the workgroup
 };
 
+// One piece of a short row, from s to every place of the token.
+template <class V>
+__device__ __forceinline__ void copy_piece(const GatherArgs& a, const uint8_t* s, uint8_t* dst, int64_t ld_dst,
+                                           const int32_t* places) {
+  const V v = *reinterpret_cast<const V*>(s);
+  for (int c = 0; c < a.topk; ++c) {
+    const int64_t p = places[c];
+    if (p >= 0 && p < a.rows_y) *reinterpret_cast<V*>(dst + p * ld_dst) = v;
+  }
+}
+
 // `lanes` lanes read a token's row in 16-byte units and write each unit to
-// every place of the token.
+// every place of the token.  The last unit of a row that is no multiple of 16
+// bytes ends with it, over the unit before (the same bytes twice): byte by
+// byte it took 16.8 us instead of 7.8 for 109 tokens of 843 bytes to six
+// places each.  Rows below 16 bytes go in pieces of eight, four, two and one.
 __global__ void __launch_bounds__(256) moe_gather_kernel(GatherArgs a) {
   const int t = static_cast<int>(threadIdx.x);
   const int per = 256 / a.lanes;
   const int64_t u = static_cast<int64_t>(blockIdx.y) * a.lanes + (t & (a.lanes - 1));
   if (u >= a.units) return;
   const bool sf = u >= a.units_x;
-  const int64_t at = 16 * (sf ? u - a.units_x : u);
-  const int64_t left = (sf ? a.sf_bytes : a.row_bytes) - at;
+  const int64_t bytes = sf ? a.sf_bytes : a.row_bytes, first = 16 * (sf ? u - a.units_x : u);
+  const int64_t at = bytes < 16 ? 0 : (first + 16 <= bytes ? first : bytes - 16);
   const uint8_t* src = (sf ? a.sfx : a.x) + at;
   uint8_t* dst = (sf ? a.sfy : a.y) + at;
   const int64_t ld_src = sf ? a.ld_sfx : a.ldx, ld_dst = sf ? a.ld_sfy : a.ldy;
@@ -241,18 +255,18 @@ __global__ void __launch_bounds__(256) moe_gather_kernel(GatherArgs a) {
        j += static_cast<int64_t>(gridDim.x) * per) {
     const uint8_t* s = src + j * ld_src;
     const int32_t* places = a.rows + j * a.topk;
-    if (left >= 16) {
+    if (bytes >= 16) {
       const v4u_a1 v = __builtin_nontemporal_load(reinterpret_cast<const v4u_a1*>(s));
       for (int c = 0; c < a.topk; ++c) {
         const int64_t p = places[c];
         if (p >= 0 && p < a.rows_y) *reinterpret_cast<v4u_a1*>(dst + p * ld_dst) = v;
       }
     } else {
-      for (int c = 0; c < a.topk; ++c) {
-        const int64_t p = places[c];
-        if (p >= 0 && p < a.rows_y)
-          for (int b = 0; b < left; ++b) dst[p * ld_dst + b] = s[b];
-      }
+      int64_t o = 0;
+      if (bytes & 8) copy_piece<v2u_a1>(a, s, dst, ld_dst, places), o = 8;
+      if (bytes & 4) copy_piece<u32_a1>(a, s + o, dst + o, ld_dst, places), o += 4;
+      if (bytes & 2) copy_piece<u16_a1>(a, s + o, dst + o, ld_dst, places), o += 2;
+      if (bytes & 1) copy_piece<uint8_t>(a, s + o, dst + o, ld_dst, places);
     }
   }
 }

@@ -247,6 +247,7 @@ __device__ __forceinline__ void row_sum(float (&v)[NV], float* slot) {
 // Eight bytes at any address.
 typedef uint32_t v2u_a1 __attribute__((ext_vector_type(2), aligned(1)));
 typedef uint32_t u32_a1 __attribute__((aligned(1)));
+typedef uint16_t u16_a1 __attribute__((aligned(1)));
 
 // Codes of eight values (already divided by their scale) in E4M3 or E5M2:
 // round to nearest even, magnitudes past the largest finite value clamped to
