@@ -62,7 +62,7 @@ def grad(m=64, n=4, s=P[0], lds=64, dy=P[1], lddy=64, dr=None, lddr=64, w=P[3], 
     (dict(m=-1), INVALID), (dict(n=-1), INVALID), (dict(types=None), INVALID), (dict(lds=1), INVALID),
     (dict(lddy=1), INVALID), (dict(lddx=1), INVALID), (dict(dr=P[2], lddr=1), INVALID), (dict(eps=-1.0), INVALID),
     (dict(s=None), INVALID), (dict(dy=None), INVALID), (dict(w=None), INVALID), (dict(dx=None), INVALID),
-    (dict(ws=None), INVALID), (dict(size=4 * 64 * 4 - 1), INVALID), (dict(ws=P[6] + 2), MISALIGNED),
+    (dict(ws=None), INVALID), (dict(size=64 * 4 - 1), INVALID), (dict(ws=P[6] + 2), MISALIGNED),
     (dict(types=("e4m3", "bf16", "bf16", "f32")), UNSUPPORTED), (dict(types=("bf16", "bf16", "i8", "f32")), UNSUPPORTED),
     (dict(types=("bf16", "bf16", "bf16", "f16")), UNSUPPORTED),
     (dict(dx=P[0] + 2), INVALID), (dict(dx=P[1], lddx=80), INVALID), (dict(dx=P[3]), INVALID),
@@ -76,7 +76,8 @@ def test_rmsnorm_backward_refusals(kw, want):
 
 
 def test_workspace_sizes():
-    assert thl.thl_rmsnorm_backward_workspace(64, 4) == 4 * 64 * 4
+    assert thl.thl_rmsnorm_backward_workspace(600, 4) == 4 * 600 * 4  # a partial row a token
+    assert thl.thl_rmsnorm_backward_workspace(64, 5) == 2 * 64 * 4  # of four short tokens
     assert thl.thl_rmsnorm_backward_workspace(64, 0) == thl.thl_rmsnorm_backward_workspace(0, 4) == 0
     assert thl.thl_rmsnorm_backward_workspace(64, 1 << 20) <= 64 * 4 * 4096  # bounded in the tokens
     assert thl.thl_moe_sort_workspace(512, 8, 64) == 0
