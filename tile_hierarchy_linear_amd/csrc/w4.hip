@@ -157,8 +157,6 @@ struct Groups {
   uint32_t z[WT == W_U4 ? (GPU + 3) / 4 : 1];
 };
 
-typedef uint16_t u16_a1 __attribute__((aligned(1)));
-
 // W words from any address.
 template <int W>
 __device__ __forceinline__ void words(const void* p, uint32_t* o) {
@@ -318,7 +316,8 @@ __device__ __forceinline__ void store_result(const W4Args& a, float v, int64_t i
 // goes down the rows, four at a time.  Two products an instruction (exact,
 // summed in fp32), one scale a lane, and the lanes' sums added in a fixed
 // order: four rows' trees share their first two levels.  The wavefronts of a
-// workgroup split K `ks` ways, and the rows otherwise.
+// workgroup split K `ks` ways, and the rows otherwise; K's slices are of equal
+// length, so that with 4,480 codes three wavefronts hold 48 pieces each.
 //
 // Matrix-core operands would have neighbouring lanes read different rows: one
 // cache access a lane instead of one for four (m = 28672, k = 8192, n = 1,
@@ -355,13 +354,14 @@ constexpr int kOneWaves = 8;
 
 // TAIL: K is not whole pieces of 32 codes.
 template <int WT, bool BF, int NT, bool TAIL>
-__global__ void __launch_bounds__(kOneWaves * 64) w4_one_kernel(W4Args a, int ks) {
+__global__ void __launch_bounds__(kOneWaves * 64) w4_one_kernel(W4Args a, int ks, int span) {
   __shared__ float part[2][kOneWaves][4][NT];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int kw = wave & (ks - 1), rg = wave / ks, groups_of_rows = kOneWaves / ks;
+  const int rg = wave / ks, kw = wave - rg * ks, groups_of_rows = static_cast<int>(blockDim.x) / (64 * ks);
   const int rows = 4 * groups_of_rows;  // a workgroup's rows at a time
-  const int pieces = a.k >> 5, slices = (pieces + 63) >> 6;
+  // K in slices of `span` pieces, a multiple of `ks` slices of equal length
+  const int pieces = a.k >> 5, slices = (pieces + span - 1) / span;
   const int blocks = (a.m + rows - 1) / rows, step = static_cast<int>(gridDim.x);
 
   // This lane's activations of a slice, and their sum.  Lanes past K's whole
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kOneWaves * 64) w4_one_kernel(W4Args a, int ks
   int x[NT][16];
   float xs[NT];
   auto load_x = [&](int slice) {
-    const int piece = 64 * slice + lane;
+    const int piece = lane < span ? span * slice + lane : pieces;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int64_t at = static_cast<int64_t>(t < a.n ? t : a.n - 1) * a.ldx + 32 * static_cast<int64_t>(piece);
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kOneWaves * 64) w4_one_kernel(W4Args a, int ks
   // branches the compiler waits for all of them at each use.
   int l_block = static_cast<int>(blockIdx.x), l_slice = kw;
   auto load_next = [&](Rows& o) {
-    int piece = 64 * l_slice + lane;
+    int piece = span * l_slice + (lane < span ? lane : 0);
     piece = piece < pieces ? piece : 0;
     const int group = static_cast<int>((32 * static_cast<int64_t>(piece)) >> a.group_shift);
     const int64_t r0 = static_cast<int64_t>(l_block) * rows + 4 * rg;
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kOneWaves * 64) w4_one_kernel(W4Args a, int ks
       if (pieces > 0) {
         load_next(ring[d ^ 1]);
         if (!one_slice) load_x(slice);
-        use(ring[d], 64 * slice + lane < pieces);
+        use(ring[d], lane < span && span * slice + lane < pieces);
       }
       slice += ks;
       if (slice < slices) continue;
@@ -859,16 +859,17 @@ template <int WT, bool BF, int NT>
 hipError_t launch_one(W4Args& a, hipStream_t st) {
   // K split over as many wavefronts as it has slices; then workgroups for
   // two a CU, each with the same number of row blocks
-  const int64_t slices = (static_cast<int64_t>(a.k) + 2047) / 2048;
+  const int pieces = a.k / 32, slices = (pieces + 63) / 64;
+  int ks = slices < kOneWaves ? (slices > 1 ? slices : 1) : kOneWaves;
+  const int rounds_k = slices > 0 ? (slices + ks - 1) / ks : 1;
+  int span = ((pieces + ks * rounds_k - 1) / (ks * rounds_k) + 7) / 8 * 8;  // whole 128-byte lines
+  if (span < 1) span = 1;
+  const int waves = kOneWaves / ks * ks, rows = 4 * (kOneWaves / ks), blocks = (a.m + rows - 1) / rows;
+  const int rounds = (blocks + 511) / 512, grid = (blocks + rounds - 1) / rounds;
   const void* f = a.k % 32 != 0 ? reinterpret_cast<const void*>(&w4_one_kernel<WT, BF, NT, true>)
                                 : reinterpret_cast<const void*>(&w4_one_kernel<WT, BF, NT, false>);
-  int ks = 1;
-  while (ks < kOneWaves && 2 * ks <= slices) ks *= 2;
-  const int rows = 4 * (kOneWaves / ks), blocks = (a.m + rows - 1) / rows;
-  const int rounds = (blocks + 511) / 512, grid = (blocks + rounds - 1) / rounds;
-  void* args[] = {&a, &ks};
-  return hipLaunchKernel(f, dim3(static_cast<unsigned>(grid)),
-                         dim3(kOneWaves * 64), args, 0, st);
+  void* args[] = {&a, &ks, &span};
+  return hipLaunchKernel(f, dim3(static_cast<unsigned>(grid)), dim3(waves * 64), args, 0, st);
 }
 
 // Token tiles of sixteen per workgroup, and workgroups along the tokens.
