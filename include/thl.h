@@ -493,8 +493,8 @@ thl_status thl_moe_combine_backward(int64_t m, int64_t n, int64_t topk, const vo
  * The epilogue is thl_gemm's (sfd unused); D may be C exactly, any other
  * overlap with D is THL_ERR_INVALID.  Products are exact in fp32; the sum of
  * a group, its zero point and scale, and the sum over groups round in fp32.
- * A token that holds an infinity or NaN gives NaN wherever integer codes meet
- * it; other tokens do not see it.  k = 0 gives act(beta*C + bias).  Any n up
+ * A token that holds an infinity or NaN gives an infinity or NaN wherever
+ * integer codes meet it; other tokens do not see it.  k = 0 gives act(beta*C + bias).  Any n up
  * to 2^21, but every 64 tokens stream the weights once more: this call is for
  * few tokens.
  *   workspace  thl_gemm_w4_workspace(m, n, k) bytes (0 for one or two tokens, and

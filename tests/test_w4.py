@@ -154,6 +154,36 @@ def test_extreme_block_scales():
     assert bool(torch.isnan(d[:, 3]).all())
 
 
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [1, 2, 3, 20, 50])
+def test_block_scales_of_the_whole_range(n, x):
+    # feature i has code 1 + i % 7 under every scale byte in turn, and token t one
+    # nonzero activation, in block t: products that are exact in fp32 wherever they are
+    # in its range, also where the weight itself is none of bf16's numbers
+    m, k = 130, 32 * 64
+    blocks = [0, 1, 2, 3, 4, 5, 124, 127, 130, 250, 251, 252, 253, 254, 9]
+    q = 1 + torch.arange(m) % 7
+    w = (q | (q << 4)).to(torch.uint8)[:, None].expand(m, k // 2).contiguous().cuda()
+    v = torch.tensor(ref.E2M1, dtype=torch.float64)[q]
+    sf = torch.full((m, 64), 127, dtype=torch.uint8)
+    xt = torch.zeros(n, k, dtype=F[x])
+    want = torch.empty(n, m, dtype=torch.float64)
+    for t in range(n):
+        b, code = (3 * t) % 64, blocks[t % len(blocks)]
+        sf[:, b] = code
+        xt[t, 32 * b + 5] = 2.0 ** (-12 if code > 127 else 6)
+        want[t] = v * float(xt[t, 32 * b + 5]) * 2.0 ** (code - 127)
+    d = torch.empty(n, m, device="cuda")
+    thl.gemm_w4(w, xt.cuda(), d, scales=sf.cuda(), group=32, type_w="e2m1")
+    torch.cuda.synchronize()
+    assert torch.equal(d.cpu().double(), want)
+    sf[3, 40] = 255
+    thl.gemm_w4(w, xt.cuda(), d, scales=sf.cuda(), group=32, type_w="e2m1")
+    torch.cuda.synchronize()
+    keep = torch.arange(m) != 3
+    assert torch.equal(d.cpu().double()[:, keep], want[:, keep]) and bool(torch.isnan(d[:, 3]).all())
+
+
 def test_infinities_stay_in_their_token():
     w, scales, zeros, xt = _make(40, 5, 300, "u4", 64)
     xt[1, 7], xt[3, 299] = float("inf"), float("nan")

@@ -4,12 +4,11 @@
 //   D(i,j) = act(alpha * sum_g s(i,g) * sum_{p in g} (q(i,p) - z(i,g)) X(p,j) + beta C(i,j) + bias_i)
 //
 // With a few tokens every weight is used a few times, so the product is a
-// stream over the weights: bound by HBM.  As in the small-M kernel, weights
-// go from memory straight into matrix-core operand registers, a whole
-// 128-byte line (256 codes) of each of 16 features per K unit, with K spread
-// over the wavefronts of a workgroup so that enough lines are in flight.
-// Tokens are the rows of the matrix-core tile, features its columns: a lane
-// then holds sums of one feature, and needs one scale a group.
+// stream over the weights: bound by HBM.  One or two tokens are multiplied
+// without matrix cores, a wavefront going down the rows (w4_one_kernel); more
+// go to the matrix cores in workgroups of 128 features (w4_many_kernel).
+// There tokens are the rows of the matrix-core tile, features its columns: a
+// lane then holds sums of one feature, and needs one scale a group.
 //
 // Codes become 16-bit floats without a conversion instruction: placed in the
 // upper mantissa bits of 16.0 an unsigned code q reads as 16 + q, exactly, in
@@ -17,12 +16,15 @@
 // the zero point, (16 + z) * sum_p X(p,j), the sum of X over a group coming
 // from a product with a matrix of ones in the same layout.  Signed codes are
 // q + 8 with their top bit turned.  E2M1 codes are converted two at a time
-// by the hardware's own instruction (exact).
+// by the hardware's own instruction (exact), under their block scale where
+// the weight then is a normal bf16.
 //
 // Every product is exact in fp32; sums within a group, its scaling and the
 // sum over groups round in fp32 like any fp32 product does.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "../../include/thl.h"
 #include "host_checks.hpp"
@@ -223,6 +225,14 @@ __device__ __forceinline__ void spread(uint32_t v, uint32_t (&o)[4]) {
   o[0] = a[0], o[1] = a[1], o[2] = b[0], o[3] = b[1];
 }
 
+// Whether any of four E8M0 scales may take an E2M1 code out of bf16's normal
+// range: 253 .. 255 and 0 .. 4 (0 and 1 would do; this way three bits are
+// dropped from b + 3, and a zero byte is what is looked for).
+__device__ __forceinline__ bool extreme(uint32_t s) {
+  const uint32_t v = (((s & 0x7f7f7f7fu) + 0x03030303u) ^ (s & 0x80808080u)) & 0xf8f8f8f8u;
+  return ((v - 0x01010101u) & ~v & 0x80808080u) != 0;
+}
+
 // A scale as stored (its low 8 or 16 bits) in fp32.
 template <int WT>
 __device__ __forceinline__ float scale_of(const W4Args& a, uint32_t b) {
@@ -264,7 +274,7 @@ __device__ __forceinline__ void load_codes_at(const uint8_t* p, int64_t left, v4
       o[d] = static_cast<int>(part);
   }
 }
-// load_codes of the partial unit at K's end.
+// A lane's codes of the partial unit at K's end, in operand order.
 __device__ __forceinline__ void load_codes_end(const W4Args& a, const uint8_t* row, int u, int g, v4i (&o)[2]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -549,7 +559,7 @@ __global__ void __launch_bounds__(256 * units_at_once(MT)) w4_many_kernel(W4Args
   constexpr int NB = 2, FW = 4, KW = units_at_once(MT);
   constexpr int PASSES = 2 / KW;  // to move sixteen rows of 32 pieces
   constexpr int LEN = 256 / GPU;  // codes per group within a unit
-  constexpr bool TURN = LEN < 128, FOLD = WT == W_E2M1 && BF;
+  constexpr bool TURN = LEN < 128;
   // Activations: [buffer][unit][tile][step][lane group][row],
   // eight a piece; piece kp of a row's unit lies at row ^ swizzle, so that neither
   // the writes (along kp) nor the reads (along the rows) meet in a bank.
@@ -643,8 +653,10 @@ __global__ void __launch_bounds__(256 * units_at_once(MT)) w4_many_kernel(W4Args
   };
 
   v4f tot[NB][MT] = {}, acc[NB][MT] = {}, xs[MT] = {};
-  // One unit: its codes in operand order, its activations as unit k2 of a buffer.
-  auto use = [&](int buffer, int k2, const v4i (&codes)[NB][2], const Groups<WT, GPU> (&groups)[NB]) {
+  // One unit: its codes in operand order, its activations as unit k2 of a
+  // buffer.  `fold`: E2M1 codes times their scale are bf16 numbers.
+  auto use = [&](int buffer, int k2, const v4i (&codes)[NB][2], const Groups<WT, GPU> (&groups)[NB], auto fold) {
+    constexpr bool FOLD = decltype(fold)::value;
     v4i wq[NB][2];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -718,7 +730,7 @@ __global__ void __launch_bounds__(256 * units_at_once(MT)) w4_many_kernel(W4Args
       }
     }
   };
-  auto turn_and_use = [&](int buffer, const v4i (&in)[NB][2], const Groups<WT, GPU> (&groups)[NB]) {
+  auto turn_and_use = [&](int buffer, const v4i (&in)[NB][2], const Groups<WT, GPU> (&groups)[NB], bool whole_range) {
     v4i codes[NB][2];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -730,7 +742,10 @@ __global__ void __launch_bounds__(256 * units_at_once(MT)) w4_many_kernel(W4Args
 #pragma unroll
       for (int h = 0; h < 2; ++h) codes[b][h] = turned[wave][b * 128 + (get ^ (4 * h))];
     __builtin_amdgcn_wave_barrier();
-    use(buffer, kw, codes, groups);
+    if constexpr (WT == W_E2M1 && BF) {
+      if (!whole_range) return use(buffer, kw, codes, groups, std::true_type{});
+    }
+    use(buffer, kw, codes, groups, std::false_type{});
   };
 
   if (len > 0) {
@@ -761,6 +776,12 @@ __global__ void __launch_bounds__(256 * units_at_once(MT)) w4_many_kernel(W4Args
           for (int j = 0; j < 4; ++j) groups[j].z[i] = o[j];
         }
       }
+      bool whole_range = false;  // weights that are not all normal bf16 numbers
+      if constexpr (WT == W_E2M1 && BF) {
+#pragma unroll
+        for (int i = 0; i < SW; ++i) whole_range |= extreme(asked.s[i]);
+        whole_range = __ballot(whole_range) != 0;
+      }
       load_scales(q + UNITS, asked);
 #pragma unroll
       for (int d = 0; d < UNITS; ++d) {
@@ -772,7 +793,7 @@ __global__ void __launch_bounds__(256 * units_at_once(MT)) w4_many_kernel(W4Args
         Groups<WT, GPU> mine[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) mine[b] = groups[d * NB + b];
-        if (KW == 1 || KW * (beg + q) + kw < whole) turn_and_use(d, ring[d], mine);
+        if (KW == 1 || KW * (beg + q) + kw < whole) turn_and_use(d, ring[d], mine, whole_range);
         load(q + 2, ring[d]);
         ++q;
       }
@@ -797,7 +818,7 @@ __global__ void __launch_bounds__(256 * units_at_once(MT)) w4_many_kernel(W4Args
         load_codes_end(a, a.w + i * a.ldw_bytes, whole, g, codes[b]);
         load_groups_end<WT, GPU>(a, i * a.ld_scales, i * a.ld_zeros, whole, groups[b]);
       }
-      use(0, 0, codes, groups);
+      use(0, 0, codes, groups, std::false_type{});
     }
   }
 
@@ -937,8 +958,6 @@ hipError_t launch_type(W4Args& a, thl_dtype w, hipStream_t st) {
   if (w == THL_E2M1X2) return launch_weights<W_E2M1, BF>(a, st);
   return w == THL_U4X2 ? launch_weights<W_U4, BF>(a, st) : launch_weights<W_I4, BF>(a, st);
 }
-
-
 
 bool big(int64_t v) { return v > INT32_MAX; }
 int64_t at_least_one(int64_t v) { return v > 1 ? v : 1; }
