@@ -286,3 +286,11 @@ def test_offsets_past_32_bits():
     thl.moe_combine(z, rows[:1], out)
     torch.cuda.synchronize()
     assert bool((out == 3.0).all())
+
+
+def test_gather_of_the_longest_token():
+    m = 1 << 26  # of four bytes: more pieces than a grid has rows of workgroups
+    x = torch.arange(m, dtype=torch.int32, device="cuda").view(1, m).view(torch.float32)
+    y = torch.zeros(2, m, device="cuda")
+    thl.moe_gather(x, torch.tensor([[1]], dtype=torch.int32, device="cuda"), y)
+    assert torch.equal(y[1:].view(torch.int32), x.view(torch.int32)) and not bool(y[0].any())

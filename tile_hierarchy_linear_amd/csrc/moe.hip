@@ -243,30 +243,31 @@ __device__ __forceinline__ void copy_piece(const GatherArgs& a, const uint8_t* s
 __global__ void __launch_bounds__(256) moe_gather_kernel(GatherArgs a) {
   const int t = static_cast<int>(threadIdx.x);
   const int per = 256 / a.lanes;
-  const int64_t u = static_cast<int64_t>(blockIdx.y) * a.lanes + (t & (a.lanes - 1));
-  if (u >= a.units) return;
-  const bool sf = u >= a.units_x;
-  const int64_t bytes = sf ? a.sf_bytes : a.row_bytes, first = 16 * (sf ? u - a.units_x : u);
-  const int64_t at = bytes < 16 ? 0 : (first + 16 <= bytes ? first : bytes - 16);
-  const uint8_t* src = (sf ? a.sfx : a.x) + at;
-  uint8_t* dst = (sf ? a.sfy : a.y) + at;
-  const int64_t ld_src = sf ? a.ld_sfx : a.ldx, ld_dst = sf ? a.ld_sfy : a.ldy;
-  for (int64_t j = static_cast<int64_t>(blockIdx.x) * per + t / a.lanes; j < a.n;
-       j += static_cast<int64_t>(gridDim.x) * per) {
-    const uint8_t* s = src + j * ld_src;
-    const int32_t* places = a.rows + j * a.topk;
-    if (bytes >= 16) {
-      const v4u_a1 v = __builtin_nontemporal_load(reinterpret_cast<const v4u_a1*>(s));
-      for (int c = 0; c < a.topk; ++c) {
-        const int64_t p = places[c];
-        if (p >= 0 && p < a.rows_y) *reinterpret_cast<v4u_a1*>(dst + p * ld_dst) = v;
+  for (int64_t u = static_cast<int64_t>(blockIdx.y) * a.lanes + (t & (a.lanes - 1)); u < a.units;
+       u += static_cast<int64_t>(gridDim.y) * a.lanes) {
+    const bool sf = u >= a.units_x;
+    const int64_t bytes = sf ? a.sf_bytes : a.row_bytes, first = 16 * (sf ? u - a.units_x : u);
+    const int64_t at = bytes < 16 ? 0 : (first + 16 <= bytes ? first : bytes - 16);
+    const uint8_t* src = (sf ? a.sfx : a.x) + at;
+    uint8_t* dst = (sf ? a.sfy : a.y) + at;
+    const int64_t ld_src = sf ? a.ld_sfx : a.ldx, ld_dst = sf ? a.ld_sfy : a.ldy;
+    for (int64_t j = static_cast<int64_t>(blockIdx.x) * per + t / a.lanes; j < a.n;
+         j += static_cast<int64_t>(gridDim.x) * per) {
+      const uint8_t* s = src + j * ld_src;
+      const int32_t* places = a.rows + j * a.topk;
+      if (bytes >= 16) {
+        const v4u_a1 v = __builtin_nontemporal_load(reinterpret_cast<const v4u_a1*>(s));
+        for (int c = 0; c < a.topk; ++c) {
+          const int64_t p = places[c];
+          if (p >= 0 && p < a.rows_y) *reinterpret_cast<v4u_a1*>(dst + p * ld_dst) = v;
+        }
+      } else {
+        int64_t o = 0;
+        if (bytes & 8) copy_piece<v2u_a1>(a, s, dst, ld_dst, places), o = 8;
+        if (bytes & 4) copy_piece<u32_a1>(a, s + o, dst + o, ld_dst, places), o += 4;
+        if (bytes & 2) copy_piece<u16_a1>(a, s + o, dst + o, ld_dst, places), o += 2;
+        if (bytes & 1) copy_piece<uint8_t>(a, s + o, dst + o, ld_dst, places);
       }
-    } else {
-      int64_t o = 0;
-      if (bytes & 8) copy_piece<v2u_a1>(a, s, dst, ld_dst, places), o = 8;
-      if (bytes & 4) copy_piece<u32_a1>(a, s + o, dst + o, ld_dst, places), o += 4;
-      if (bytes & 2) copy_piece<u16_a1>(a, s + o, dst + o, ld_dst, places), o += 2;
-      if (bytes & 1) copy_piece<uint8_t>(a, s + o, dst + o, ld_dst, places);
     }
   }
 }
@@ -425,14 +426,14 @@ int lanes_for(int64_t units) {
   return l;
 }
 
-// Tokens in x (each workgroup then walks on), pieces of a token in y.
-bool token_grid(int64_t n, int64_t units, int lanes, dim3* g) {
+// Tokens in x (each workgroup then walks on), pieces of a token in y (a
+// gather of 2^26 features of four bytes walks on there too; combine's pieces,
+// of eight features, are 2^15 workgroups at most).
+dim3 token_grid(int64_t n, int64_t units, int lanes) {
   const int64_t per = 256 / lanes, gy = (units + lanes - 1) / lanes;
   int64_t gx = (n + per - 1) / per;
   if (gx > 65536) gx = 65536;
-  if (gy > 65535) return false;
-  *g = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
-  return true;
+  return dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy < 65535 ? gy : 65535));
 }
 
 // A token of up to 1,024 features goes to one wavefront, longer ones to four.
@@ -598,8 +599,7 @@ thl_status thl_moe_gather(int64_t m, int64_t n, int64_t topk, const void* X, int
   a.row_bytes = bytes_of(type, m), a.sf_bytes = sfx ? (m + 31) / 32 : 0;
   a.units_x = (a.row_bytes + 15) / 16, a.units = a.units_x + (a.sf_bytes + 15) / 16;
   a.lanes = lanes_for(a.units);
-  dim3 grid;
-  if (!token_grid(n, a.units, a.lanes, &grid)) return THL_ERR_UNSUPPORTED;
+  const dim3 grid = token_grid(n, a.units, a.lanes);
   return launch(reinterpret_cast<const void*>(&moe_gather_kernel), grid, 256, &a, stream) == hipSuccess ? THL_OK
                                                                                                          : THL_ERR_HIP;
 }
@@ -626,8 +626,7 @@ thl_status thl_moe_combine(int64_t m, int64_t n, int64_t topk, const void* X, in
   a.m = static_cast<int32_t>(m), a.topk = static_cast<int32_t>(topk), a.x_type = type_x, a.y_type = type_y;
   const int64_t units = (m + 7) / 8;
   a.lanes = lanes_for(units);
-  dim3 grid;
-  if (!token_grid(n, units, a.lanes, &grid)) return THL_ERR_UNSUPPORTED;
+  const dim3 grid = token_grid(n, units, a.lanes);
   if (rows_x == 0) a.topk = 0;  // no row to add
   const hipError_t e = type_x == THL_F32 ? launch_combine<4>(a, grid, stream) : launch_combine<2>(a, grid, stream);
   return e == hipSuccess ? THL_OK : THL_ERR_HIP;
