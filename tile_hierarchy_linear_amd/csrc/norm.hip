@@ -15,6 +15,11 @@
 // lane, so the values that the sum of squares needs are still there when the
 // outputs are formed.  Only tokens of more than 16,384 features are read
 // twice (the second time from L2).
+//
+// Measured on bf16: the norm of 16,384 tokens of 8,192 features with residual
+// 187 us (5.7 TB/s; a large copy runs at 5.0), of one token 4.4 us (a launch
+// alone takes 3.9); the gradient of 8,192 tokens of 4,096 features 52.8 us
+// (5.1 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -9,6 +9,9 @@
 // go to the matrix cores in workgroups of 128 features (w4_many_kernel).
 // There tokens are the rows of the matrix-core tile, features its columns: a
 // lane then holds sums of one feature, and needs one scale a group.
+// Measured: one token, signed codes in groups of 128, m = 28672, k = 8192 23.6
+// us (5.1 TB/s); 48 tokens, MX fp4 weights, m = k = 8192 21.9 us, of which 6
+// would be the stream's.
 //
 // Codes become 16-bit floats without a conversion instruction: placed in the
 // upper mantissa bits of 16.0 an unsigned code q reads as 16 + q, exactly, in
