@@ -245,3 +245,24 @@ def test_torch_form_refusals(bad):
             thl.gemm_w4(w, xt.float(), d, **kw)
         else:
             thl.gemm_w4(w, xt, d, beta=1.0, **kw)
+
+
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [1, 2, 3, 40])
+@pytest.mark.parametrize("type_w,group", [("u4", 32), ("i4", 128), ("e2m1", 32)])
+def test_subnormal_activations(type_w, group, x, n):
+    # one nonzero activation a token, below the format's normal numbers: exact in fp32
+    m, k = 40, 1024
+    w, _, zeros, _ = _make(m, n, k, type_w, group, x)
+    scales = torch.full((m, k // group), 127 if type_w == "e2m1" else 1.0,
+                        dtype=torch.uint8 if type_w == "e2m1" else F[x], device="cuda")
+    xt = torch.zeros(n, k, dtype=F[x])
+    for t in range(n):
+        xt[t, (37 * t + 5) % k] = (3 + t) * (2.0 ** -24 if x == "f16" else 2.0 ** -133)
+    assert bool((xt.abs().amax(dim=1) < torch.finfo(F[x]).tiny).all()) and bool((xt.abs().amax(dim=1) > 0).all())
+    up = 2.0 ** 20  # the sums themselves stay normal in fp32
+    d = torch.empty(n, m, device="cuda")
+    thl.gemm_w4(w, xt.cuda(), d, scales=scales, group=group, type_w=type_w, zeros=zeros, alpha=up)
+    torch.cuda.synchronize()
+    want, _ = ref.gemm_w4(w, type_w, scales, group, zeros, xt.cuda(), k)
+    assert torch.equal(d.double().cpu(), want.cpu() * up)
