@@ -122,19 +122,27 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(SortArgs a) {
     }
   }
   if (a.blocks > 1) {
-    const int n = a.blocks * a.experts;
-    for (int i = t; i < n; i += 4 * kSortThreads) {
-      int c[4];
+    // A thread adds one expert's counts of every `slices`-th workgroup.
+    const int cols = a.experts < kSortThreads ? a.experts : kSortThreads, slices = kSortThreads / cols;
+    const int sl = t / cols;
+    for (int e = sl < slices ? t - sl * cols : a.experts; e < a.experts; e += cols) {
+      int sum = 0, sum_before = 0;
+      for (int b = sl; b < a.blocks; b += 16 * slices) {
+        int c[16];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) c[q] = a.counts[i + q * kSortThreads < n ? i + q * kSortThreads : n - 1];
+        for (int q = 0; q < 16; ++q) {
+          const int at = b + q * slices < a.blocks ? b + q * slices : b;
+          c[q] = a.counts[static_cast<int64_t>(at) * a.experts + e];
+        }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int at = i + q * kSortThreads, b = at / a.experts, e = at - b * a.experts;
-        if (at < n && c[q] != 0) {
-          atomicAdd(&all[e], c[q]);
-          if (b < me) atomicAdd(&before[e], c[q]);
+        for (int q = 0; q < 16; ++q) {
+          const int at = b + q * slices;
+          sum += at < a.blocks ? c[q] : 0;
+          sum_before += at < me && at < a.blocks ? c[q] : 0;
         }
       }
+      if (sum != 0) atomicAdd(&all[e], sum);
+      if (sum_before != 0) atomicAdd(&before[e], sum_before);
     }
   }
   __syncthreads();
