@@ -242,6 +242,23 @@ def test_backward_many_tokens():
     _grad(1500, 16392, dres=False)  # several tokens a workgroup on the path that reads twice
 
 
+@pytest.mark.parametrize("n,m", [(4099, 227), (5000, 600), (4200, 1500), (600, 5003), (520, 8192), (300, 9001), (270, 16384)])
+@pytest.mark.parametrize("g", ["bf16", "f32"])
+def test_backward_more_tokens_than_workgroups(n, m, g):
+    _grad(n, m, s="f32" if g == "f32" else "bf16", g=g, seed=n)
+
+
+@pytest.mark.parametrize("n,m", [(300, 9001), (2, 6000)])
+def test_backward_long_tokens_in_place(n, m):
+    st, dy, dr, w, dx, dw = _grad(n, m, seed=5)
+    for out in (dy, dr, st):
+        keep, dw2 = out.clone(), torch.empty_like(dw)
+        thl.rmsnorm_backward(st, dy, w, out, dw2, eps=EPS, dres=dr)
+        torch.cuda.synchronize()
+        assert torch.equal(out, dx) and torch.equal(dw2, dw)
+        out.copy_(keep)
+
+
 def test_backward_without_dw_and_in_place():
     st, dy, dr, w, dx, _ = _grad(600, 1000)
     thl.rmsnorm_backward(st, dy, w, dy, None, eps=EPS, dres=dr)  # dx over dy

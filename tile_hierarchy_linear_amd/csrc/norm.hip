@@ -253,9 +253,24 @@ __global__ void __launch_bounds__(WPR * tokens_at_once(WPR) * 64) rmsnorm_grad_k
   float* part = a.part ? a.part + static_cast<int64_t>(blockIdx.x) * m : nullptr;
   if constexpr (CH > 0) {
     RawAny wr[NC];
-    float acc[NC][8] = {};
+    // dw's sums: of one run a lane in registers, of two in LDS, and the weights
+    // in fp32 in registers instead (4,096 tokens of 8,192 bf16 features: 47 us;
+    // 63 with one run a lane on twice the wavefronts; 2,048 of 16,384: 54 us,
+    // 100 with everything in registers, of which 30 spill)
+    constexpr bool IN_LDS = NC > 1;
+    float acc[IN_LDS ? 1 : NC][8] = {};
+    __shared__ __attribute__((aligned(16))) v4f held[IN_LDS ? 2 * NC * T : 1];
+    if constexpr (IN_LDS) {
+#pragma unroll
+      for (int c = 0; c < 2 * NC; ++c) held[c * T + t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
 #pragma unroll
     for (int c = 0; c < NC; ++c) wr[c] = load_any<RUNS>(a.w, a.w_type, 8 * (t + T * c), m);
+    float w[NC][8];
+    if constexpr (IN_LDS) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) any_f8<RUNS>(wr[c], a.w_type, 8 * (t + T * c), m, w[c]);
+    }
     // without a gradient past the norm, dy is loaded in its place and not used
     const void* dr = a.dr ? a.dr : a.dy;
     const int64_t lddr = a.dr ? a.lddr : a.lddy;
@@ -270,7 +285,7 @@ __global__ void __launch_bounds__(WPR * tokens_at_once(WPR) * 64) rmsnorm_grad_k
         gr[c] = load_run<GB, RUNS>(a.dy, row * a.lddy, e, m);
         rr[c] = load_run<GB, RUNS>(dr, row * lddr, e, m);
       }
-      float s[NC][8], g[NC][8], w[NC][8], sum[2] = {0.0f, 0.0f};
+      float s[NC][8], g[NC][8], sum[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int e = 8 * (t + T * c);
@@ -278,7 +293,7 @@ __global__ void __launch_bounds__(WPR * tokens_at_once(WPR) * 64) rmsnorm_grad_k
         settle<GB, RUNS>(gr[c], e, m);
         to_f8<SB>(sr[c], s_bf, s[c]);
         to_f8<GB>(gr[c], g_bf, g[c]);
-        any_f8<RUNS>(wr[c], a.w_type, e, m, w[c]);
+        if constexpr (!IN_LDS) any_f8<RUNS>(wr[c], a.w_type, e, m, w[c]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           sum[0] += s[c][i] * s[c][i];
@@ -300,8 +315,13 @@ __global__ void __launch_bounds__(WPR * tokens_at_once(WPR) * 64) rmsnorm_grad_k
         float d[8] = {}, h[8];
         if (a.dr) to_f8<GB>(rr[c], g_bf, d);
         emit(row, 8 * (t + T * c), s[c], g[c], w[c], d, rho, mean, h);
+        if constexpr (IN_LDS) {
+          held[2 * c * T + t] += v4f{h[0], h[1], h[2], h[3]};
+          held[(2 * c + 1) * T + t] += v4f{h[4], h[5], h[6], h[7]};
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[c][i] += h[i];
+          for (int i = 0; i < 8; ++i) acc[c][i] += h[i];
+        }
       }
     }
     if (!part) return;
@@ -322,7 +342,10 @@ __global__ void __launch_bounds__(WPR * tokens_at_once(WPR) * 64) rmsnorm_grad_k
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int e = 8 * (t + T * c);
-        if (e < m) store8_f(part, THL_F32, e, acc[c], m - e < 8 ? m - e : 8);
+        float p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = IN_LDS ? held[IN_LDS ? (2 * c + i / 4) * T + t : 0][i % 4] : acc[IN_LDS ? 0 : c][i];
+        if (e < m) store8_f(part, THL_F32, e, p, m - e < 8 ? m - e : 8);
       }
     }
   } else {
@@ -443,10 +466,14 @@ hipError_t launch_norm(NormArgs& a, hipStream_t st) {
 // device, few enough that the partial rows stay a small part of the traffic.
 // Short tokens leave few bytes in flight a workgroup and want more of them:
 // 16,384 tokens of 1,024 bf16 features take 33.8 us with 2,048 rows on two
-// wavefronts each and 41.5 with 1,024 rows on four.
+// wavefronts each and 41.5 with 1,024 rows on four.  From 8,193 to 16,384 a
+// workgroup fills a compute unit, and 256 are all that run at a time: 2,048
+// tokens of 16,384 features take 61 us and 70 with 512 rows.
 int64_t grad_rows(int64_t m, int64_t n) {
   const int64_t tokens = m <= 512 ? (n + tokens_at_once(1) - 1) / tokens_at_once(1) : n;
-  const int64_t most = n < 4096 ? 512 : (m <= 1024 ? 2048 : (m <= 2048 ? 1024 : 512));
+  int64_t most = 512;
+  if (m <= 2048 && n >= 4096) most = m <= 1024 ? 2048 : 1024;
+  if (m > 8192 && m <= 16384) most = 256;
   return tokens < most ? tokens : most;
 }
 
@@ -460,7 +487,7 @@ hipError_t launch_grad(NormGradArgs& a, int64_t grid, hipStream_t st) {
     if (a.m <= 1024) THL_GRAD(2, 1);
     if (a.m <= 2048) THL_GRAD(4, 1);
     if (a.m <= 4096) THL_GRAD(8, 1);
-    if (a.m <= 8192) THL_GRAD(16, 1);
+    if (a.m <= 8192) THL_GRAD(8, 2);
     if (a.m <= 16384) THL_GRAD(16, 2);
     THL_GRAD(16, 0);
   }
