@@ -368,10 +368,10 @@ thl_status thl_gemm_grouped(int64_t count, const thl_group_problem* problems,
  * unrounded s.  R = NULL: no residual (s = x; S must be NULL).  S = NULL with
  * a residual: the sum is not kept.
  *   types  x: F32, F16 or BF16.  r (R and S): x's type or F32.  w: F32, F16 or
- *          BF16.  y: F32, F16 or BF16; E4M3 or E5M2 with sfy = NULL: y /
- *          y_scale, magnitudes past the largest finite value clamped to it
- *          (y_scale is the product's a_scale or b_scale; 1 for every other
- *          form); E4M3, E5M2 or E2M1X2 with sfy: MX blocks of 32 consecutive
+ *          BF16.  y: F32, F16 or BF16; E4M3 or E5M2 with sfy = NULL: y *
+ *          (1 / y_scale), the reciprocal and the product rounded in fp32 each,
+ *          magnitudes past the largest finite value clamped to it (y_scale is
+ *          the product's a_scale or b_scale; 1 for every other form); E4M3, E5M2 or E2M1X2 with sfy: MX blocks of 32 consecutive
  *          features by thl_gemm's MX-output rule, SFY(b, j) at
  *          sfy[j*ld_sfy + b], ld_sfy >= ceil(m/32) (a product that reads them
  *          as sfa or sfb wants a multiple of 16), E2M1X2 with ldy even.

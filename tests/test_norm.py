@@ -321,3 +321,40 @@ def test_torch_form_refusals(bad):
             thl.rmsnorm(x, w, y, residual_out=y)
         else:
             thl.rmsnorm_backward(x, x, w, torch.empty(4, 64, device="cuda", dtype=torch.float16))
+
+
+@pytest.mark.parametrize("y", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("m", [1024, 1003, 16500])  # 1003: a ragged row; 16,500: the token read twice
+def test_one_scale_is_a_product_with_its_reciprocal(y, m):
+    """x all ones and eps = 0: the norm of ones is exactly w, so y is w * (1 / scale) in fp32, rounded once more.  The
+    weights are where the quotient lies on or next to a midpoint of two codes, which a division would now and then
+    leave to the other side."""
+    top = ref.TOP[y]
+    codes = torch.arange(1, 256, dtype=torch.uint8).view(F[y]).float()
+    codes = torch.sort(codes[torch.isfinite(codes) & (codes > 0)]).values
+    mids = (codes[1:].double() + codes[:-1].double()) / 2
+    x, differ = torch.ones(2, m, device="cuda"), 0  # codes that a division gives otherwise
+    for scale in (0.02, 0.0123, 0.7, 3.0, 1.7e-30, 3.1e29):
+        s = torch.tensor(scale, dtype=torch.float32)
+        near = (mids * s.double()).float()
+        w = torch.cat([near, torch.nextafter(near, torch.tensor(0.0)), -torch.nextafter(near, torch.tensor(torch.inf)),
+                       torch.tensor([0.0, -0.0, 3e38, -3e38, torch.inf, 1e-45, 1e-38])])
+        w = w.repeat(-(-m // w.numel()))[:m]
+        q = w * (1 / s)  # both rounded in fp32
+        want = q.clamp(-top, top).to(F[y]).view(torch.uint8)
+        differ += int(((w / s).clamp(-top, top).to(F[y]).view(torch.uint8) != want).sum())
+        got = torch.empty(2, m, dtype=F[y], device="cuda")
+        thl.rmsnorm(x, w.cuda(), got, eps=0.0, scale=float(s))
+        torch.cuda.synchronize()
+        got = got.view(torch.uint8).cpu()
+        assert torch.equal(got[0], want) and torch.equal(got[1], want), scale
+    assert differ > 0  # a division is something else
+
+
+def test_one_scale_keeps_nan():
+    w = torch.ones(64, device="cuda")
+    w[5] = float("nan")
+    y = torch.empty(1, 64, dtype=torch.float8_e4m3fn, device="cuda")
+    thl.rmsnorm(torch.ones(1, 64, device="cuda"), w, y, eps=0.0, scale=0.3)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(y[0, 5].float())) and not bool(torch.isnan(y.float()[0, torch.arange(64) != 5]).any())

@@ -387,7 +387,7 @@ if _torch is not None:
 
 def rmsnorm(x, w, y, *, eps=1e-6, residual=None, residual_out=None, scale=1.0, sf=None):
     """y = the root-mean-square norm of x (+ residual) times w, in y's format; the sum goes to residual_out.
-    An fp8 y holds y / scale, or MX blocks when sf takes their E8M0 scales; a uint8 y of ceil(features / 2)
+    An fp8 y holds y * (1 / scale), or MX blocks when sf takes their E8M0 scales; a uint8 y of ceil(features / 2)
     columns holds E2M1 MX blocks.  Returns y."""
     status = _ops.rmsnorm(x, w, y, eps, residual, residual_out, scale, sf)
     if status:

@@ -59,6 +59,10 @@ __device__ __forceinline__ void store_out(const NormArgs& a, int64_t row, int e,
   }
   uint8_t* y = static_cast<uint8_t*>(a.y);
   if (a.y_mode == Y_FP8) {
+    // times the rounded 1 / scale: a quotient next to the midpoint of two codes
+    // may take the other one.  Divided instead, 8,192 tokens of 4,096 bf16
+    // features take 28.0 us for 23.9, 16,384 of 16,384 to e5m2 226 for 174 (25.5
+    // and 187 with the product corrected by its remainder).
     float q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = v[i] * a.inv_scale;
