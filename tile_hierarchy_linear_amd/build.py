@@ -1,5 +1,5 @@
 """Build libthl.so (HIP kernels for gfx950 + host C++) in-tree with hipcc, and
-_torch_ops.so (host C++ only) where torch is installed."""
+_torch_ops.so (host C++ only) where a torch with its HIP libraries is."""
 from __future__ import annotations
 
 import importlib.util
@@ -35,6 +35,8 @@ def build_torch_ops() -> None:
     if spec is None:
         return
     torch = list(spec.submodule_search_locations)[0]
+    if not os.path.exists(os.path.join(torch, "lib", "libc10_hip.so")):  # a torch without GPUs: no tensors to take
+        return
     rocm = os.path.dirname(os.path.dirname(os.path.realpath(HIPCC)))
     tmp = TORCH_OPS + ".tmp"
     subprocess.check_call(
