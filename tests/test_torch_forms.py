@@ -1,12 +1,55 @@
 """The torch-tensor forms beside torch itself."""
+import os
 import subprocess
+import sys
 
 import pytest
 
 torch = pytest.importorskip("torch")
 
+import tile_hierarchy_linear_amd as thl
+
+PKG = os.path.dirname(os.path.abspath(thl.__file__))
+
 
 # ------------------------------------------------------------------ a torch without the host module
+
+def _package_without_the_module(tmp_path):
+    """A copy of the package (its library linked) that has no _torch_ops.so."""
+    pkg = tmp_path / "tile_hierarchy_linear_amd"
+    pkg.mkdir()
+    for name in os.listdir(PKG):
+        if name.endswith(".py") or name == "libthl.so":
+            os.symlink(os.path.join(PKG, name), pkg / name)
+    return pkg
+
+
+_USE = """
+import tile_hierarchy_linear_amd as thl
+assert thl.__file__.startswith({root!r}), thl.__file__
+assert thl.thl_status_string(0) and thl.thl_variant_count() > 0
+assert thl.thl_rmsnorm(0, 0, None, 1, None, 1, None, 1, None, 1e-6, 1.0, None, 1, None, 1,
+                       thl.thl_norm_types(0, 0, 0, 0)) == 0
+try:
+    thl.rmsnorm(None, None, None)
+except ImportError as e:
+    assert "_torch_ops" in str(e), e
+else:
+    raise AssertionError("rmsnorm took its arguments")
+print("done")
+"""
+
+
+@pytest.mark.parametrize("broken", ["absent", "another"])
+def test_the_library_loads_without_the_torch_forms(tmp_path, broken):
+    pkg = _package_without_the_module(tmp_path)
+    if broken == "another":  # one that this torch cannot load
+        (pkg / "_torch_ops.so").write_bytes(b"no library")
+    # run from a path-loaded copy: the C binding works, a torch form says what it misses
+    code = f"import sys; sys.path.insert(0, {str(tmp_path)!r})\n" + _USE.format(root=str(tmp_path))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=tmp_path, timeout=300)
+    assert r.returncode == 0 and r.stdout.endswith("done\n"), r.stderr
+
 
 def test_build_without_torch_s_hip_libraries(tmp_path, monkeypatch):
     from importlib.machinery import ModuleSpec

@@ -5,7 +5,8 @@ weights), and the Shape:Stride layout module.
 Argument marshalling only: every step of the GEMM and of the operators runs
 in the library's HIP kernels, and the layout algebra in its C++.  The names
 match the C entry points of ``include/thl.h``.  Importing this module fails
-loudly when the built library is missing; there is no fallback.
+loudly when the built library is missing, and the torch-tensor forms when the
+host module behind them does not load; there is no fallback.
 """
 from __future__ import annotations
 
@@ -66,18 +67,16 @@ class thl_group_scales(ctypes.Structure):
                 ("ld_zeros", ctypes.c_int64), ("group", ctypes.c_int64), ("type", ctypes.c_int)]
 
 
-try:
-    import torch as _torch
-except ImportError:
-    _torch = None
-
-
 def _load():
     # One HIP runtime per process.  torch ships its own libamdhip64 and asks
     # for it by its unversioned name, so loading libthl first (which pulls in
     # the system libamdhip64.so.7) would leave two runtimes in the process and
     # device pointers from one invalid in the other.  Importing torch first
-    # (above) makes libthl bind to torch's runtime.
+    # makes libthl bind to torch's runtime.
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        pass
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run __graft_entry__.build() "
                           "or python tile_hierarchy_linear_amd/build.py")
@@ -378,11 +377,23 @@ def thl_gemm_w4(m, n, k, W, ldw, scales, X, ldx, C, ldc, D, ldd, alpha, beta, dt
 # device and ThlError for what the library refuses.  The tensors are read and
 # checked in csrc/torch_ops.cpp: in Python that took as long as the launch.
 
-if _torch is not None:
-    if not os.path.exists(os.path.join(_HERE, "_torch_ops.so")):
-        raise ImportError(f"{os.path.join(_HERE, '_torch_ops.so')} is not built; run __graft_entry__.build() "
-                          "or python tile_hierarchy_linear_amd/build.py")
+
+class _NoTorchForms:
+    """In place of the host module where it does not load: each form raises."""
+
+    def __init__(self, reason):
+        self._reason = reason
+
+    def __getattr__(self, name):
+        raise ImportError(f"thl.{name} takes torch tensors through {os.path.join(_HERE, '_torch_ops.so')}, which does "
+                          "not load; run __graft_entry__.build() or python tile_hierarchy_linear_amd/build.py "
+                          f"({self._reason})")
+
+
+try:
     from . import _torch_ops as _ops
+except ImportError as e:  # not built, or for another torch; the C entry points above do not need it
+    _ops = _NoTorchForms(str(e))
 
 
 def rmsnorm(x, w, y, *, eps=1e-6, residual=None, residual_out=None, scale=1.0, sf=None):
