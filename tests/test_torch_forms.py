@@ -76,3 +76,32 @@ def test_build_without_torch_s_hip_libraries(tmp_path, monkeypatch):
     with pytest.raises(subprocess.CalledProcessError):
         build.build_torch_ops()  # with them it is built, and a failure is one
     assert len(started) == 1
+
+
+@pytest.mark.parametrize("symbol", ["PyModule_Create2", "thl_not_a_symbol_of_torch"])
+def test_build_fails_where_the_module_would_not_load(tmp_path, monkeypatch, symbol):
+    from tile_hierarchy_linear_amd import build
+
+    (tmp_path / "torch_ops.cpp").write_text(f'extern "C" void {symbol}(); extern "C" void use() {{ {symbol}(); }}\n')
+    monkeypatch.setattr(build, "CSRC", str(tmp_path))
+    monkeypatch.setattr(build, "TORCH_OPS", str(tmp_path / "_torch_ops.so"))
+    if symbol.startswith("thl"):
+        with pytest.raises(subprocess.CalledProcessError):
+            build.build_torch_ops()
+    else:
+        build.build_torch_ops()
+    assert os.path.exists(tmp_path / "_torch_ops.so") == (not symbol.startswith("thl"))
+
+
+def test_a_module_for_another_torch_goes(tmp_path, monkeypatch):
+    from importlib.machinery import ModuleSpec
+
+    from tile_hierarchy_linear_amd import build
+
+    spec = ModuleSpec("torch", None, is_package=True)
+    spec.submodule_search_locations = [str(tmp_path / "torch")]
+    monkeypatch.setattr(build.importlib.util, "find_spec", lambda name: spec)
+    monkeypatch.setattr(build, "TORCH_OPS", str(tmp_path / "_torch_ops.so"))
+    (tmp_path / "_torch_ops.so").write_bytes(b"built with a HIP torch")
+    build.build_torch_ops()
+    assert not os.path.exists(tmp_path / "_torch_ops.so")

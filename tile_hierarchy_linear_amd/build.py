@@ -36,6 +36,8 @@ def build_torch_ops() -> None:
         return
     torch = list(spec.submodule_search_locations)[0]
     if not os.path.exists(os.path.join(torch, "lib", "libc10_hip.so")):  # a torch without GPUs: no tensors to take
+        if os.path.exists(TORCH_OPS):  # built for another torch
+            os.remove(TORCH_OPS)
         return
     rocm = os.path.dirname(os.path.dirname(os.path.realpath(HIPCC)))
     tmp = TORCH_OPS + ".tmp"
@@ -45,6 +47,9 @@ def build_torch_ops() -> None:
          "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "torch_ops.cpp"), "-o", tmp,
          "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-L" + HERE,
          "-l:libthl.so", "-Wl,-rpath,$ORIGIN"])
+    # a symbol that torch does not export shows here, not at a user's first call
+    load = f"import ctypes, os, torch; ctypes.CDLL({os.path.abspath(tmp)!r}, os.RTLD_NOW)"
+    subprocess.check_call([sys.executable, "-c", load])
     os.replace(tmp, TORCH_OPS)
 
 
