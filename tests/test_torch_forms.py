@@ -12,6 +12,28 @@ import tile_hierarchy_linear_amd as thl
 PKG = os.path.dirname(os.path.abspath(thl.__file__))
 
 
+# ------------------------------------------------------------------ out of memory
+
+@pytest.mark.gpu
+def test_a_workspace_that_does_not_fit_raises_torch_s_error():
+    m = 1 << 24
+    s, dy, dx = (torch.zeros(8, m, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    w, dw = torch.ones(m, device="cuda"), torch.zeros(m, device="cuda")
+    assert thl.thl_rmsnorm_backward_workspace(m, 8) == 8 * m * 4
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (64 << 20)) / total)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            thl.rmsnorm_backward(s, dy, w, dx, dw)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    thl.rmsnorm_backward(s, dy, w, dx, dw)  # and goes on
+    torch.cuda.synchronize()
+    assert not bool(dw.any())
+
+
 # ------------------------------------------------------------------ a torch without the host module
 
 def _package_without_the_module(tmp_path):

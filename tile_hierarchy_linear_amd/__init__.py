@@ -374,8 +374,9 @@ def thl_gemm_w4(m, n, k, W, ldw, scales, X, ldx, C, ldc, D, ldd, alpha, beta, dt
 # caller made, so that serving loops and graphs reuse them.  They issue on the
 # current stream of the tensors' device, take their workspaces from torch on
 # that stream, and raise ValueError for a tensor of the wrong shape, type or
-# device and ThlError for what the library refuses.  The tensors are read and
-# checked in csrc/torch_ops.cpp: in Python that took as long as the launch.
+# device, ThlError for what the library refuses and torch.OutOfMemoryError
+# where a workspace does not fit.  The tensors are read and checked in
+# csrc/torch_ops.cpp: in Python that took as long as the launch.
 
 
 class _NoTorchForms:

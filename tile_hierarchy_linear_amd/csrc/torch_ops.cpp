@@ -8,7 +8,8 @@
 // a call, 3 of them the launch); here they are a fraction of a microsecond.
 //
 // Every function returns the thl_status of its call; wrong tensors raise
-// ValueError and nothing is launched.
+// ValueError, a workspace that does not fit torch.OutOfMemoryError, and nothing
+// is launched.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -382,6 +383,16 @@ thl_status gemm_w4(PyObject* const* a) {
                      need, l.stream);
 }
 
+// torch.OutOfMemoryError, which programs catch to go on with less (torch does
+// not export its C++ handle).
+void out_of_memory(const char* what) {
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+  if (type) PyErr_SetString(type, what);
+  Py_XDECREF(type);
+  Py_XDECREF(torch);
+}
+
 // One Python function: N positional arguments, errors as exceptions.
 template <thl_status (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -393,7 +404,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   } catch (const Refused& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
   } catch (const c10::OutOfMemoryError& e) {
-    PyErr_SetString(PyExc_MemoryError, e.what_without_backtrace());
+    out_of_memory(e.what_without_backtrace());
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {
