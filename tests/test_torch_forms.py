@@ -12,6 +12,116 @@ import tile_hierarchy_linear_amd as thl
 PKG = os.path.dirname(os.path.abspath(thl.__file__))
 
 
+def _calls(device):
+    """One call of every form: its function, its tensors by name, its other arguments, and the names it writes."""
+    f, i, u = torch.float32, torch.int32, torch.uint8
+
+    def t(*shape, dtype=f):
+        return torch.zeros(*shape, dtype=dtype, device=device)
+
+    places = torch.arange(8, dtype=i, device=device).reshape(4, 2)
+    return {
+        "rmsnorm": (thl.rmsnorm, dict(x=t(4, 64), w=t(64), y=t(4, 64), residual=t(4, 64), residual_out=t(4, 64)), {},
+                    ("y", "residual_out")),
+        "rmsnorm_mx": (thl.rmsnorm, dict(x=t(4, 64), w=t(64), y=t(4, 64, dtype=torch.float8_e4m3fn),
+                                         sf=t(4, 16, dtype=u)), {}, ("y", "sf")),
+        "rmsnorm_backward": (thl.rmsnorm_backward, dict(s=t(4, 64), dy=t(4, 64), w=t(64), dx=t(4, 64), dw=t(64),
+                                                        dres=t(4, 64)), {}, ("dx", "dw")),
+        "moe_sort": (thl.moe_sort, dict(ids=t(4, 2, dtype=i), rows=t(4, 2, dtype=i), offsets=t(6, dtype=i),
+                                        order=t(8, dtype=i)), dict(experts=5), ("rows", "offsets", "order")),
+        "moe_gather": (thl.moe_gather, dict(x=t(4, 64), rows=places, y=t(8, 64)), {}, ("y",)),
+        "moe_gather_mx": (thl.moe_gather, dict(x=t(4, 64, dtype=u), rows=places, y=t(8, 64, dtype=u),
+                                               sf=t(4, 16, dtype=u), sf_y=t(8, 16, dtype=u)), {}, ("y", "sf_y")),
+        "moe_combine": (thl.moe_combine, dict(x=t(8, 64), rows=places, y=t(4, 64), weights=t(4, 2)), {},
+                        ("y",)),
+        "moe_combine_backward": (thl.moe_combine_backward,
+                                 dict(dy=t(4, 64), x=t(8, 64), rows=places, weights=t(4, 2), dx=t(8, 64),
+                                      dweights=t(4, 2)), {}, ("dx", "dweights")),
+        "gemm_w4": (thl.gemm_w4, dict(w=t(32, 64, dtype=u), x=t(3, 128, dtype=torch.float16), d=t(3, 32),
+                                      scales=t(32, 1, dtype=torch.float16), zeros=t(32, 1, dtype=u), c=t(3, 32),
+                                      bias=t(32)), dict(group=128, beta=1.0), ("d",)),
+    }
+
+
+FORMS = ["rmsnorm", "rmsnorm_mx", "rmsnorm_backward", "moe_sort", "moe_gather", "moe_gather_mx", "moe_combine",
+         "moe_combine_backward", "gemm_w4"]
+
+
+# ------------------------------------------------------------------ autograd
+
+def _floats(form, device):
+    return [k for k, v in _calls(device)[form][1].items() if v.dtype in (torch.float32, torch.float16)]
+
+
+def _refused_where_recorded(form, device, names):
+    for name in names:
+        call, tensors, rest, _ = _calls(device)[form]
+        tensors[name].requires_grad_()
+        with pytest.raises(ValueError, match=f"{name}: requires a gradient"):
+            call(**tensors, **rest)
+        call, tensors, rest, _ = _calls(device)[form]
+        with torch.autograd.forward_ad.dual_level():
+            tensors[name] = torch.autograd.forward_ad.make_dual(tensors[name], torch.ones_like(tensors[name]))
+            with pytest.raises(ValueError, match=f"{name}: requires a gradient"):
+                call(**tensors, **rest)
+
+
+@pytest.mark.parametrize("form,first", [
+    ("rmsnorm", "x"), ("rmsnorm", "w"), ("rmsnorm", "y"), ("rmsnorm_backward", "s"), ("rmsnorm_backward", "dy"),
+    ("moe_gather", "x"), ("moe_combine", "x"), ("moe_combine_backward", "dy"), ("gemm_w4", "x"), ("gemm_w4", "scales")])
+def test_a_tensor_that_requires_a_gradient_is_refused(form, first):
+    # (seen before the device, so that it shows without a GPU)
+    _refused_where_recorded(form, "cpu", [first])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", FORMS)
+def test_every_tensor_that_requires_a_gradient_is_refused(form):
+    _refused_where_recorded(form, "cuda", _floats(form, "cuda"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", FORMS)
+def test_such_tensors_are_taken_where_nothing_is_recorded(form):
+    call, tensors, rest, written = _calls("cuda")[form]
+    for name in _floats(form, "cuda"):
+        tensors[name].requires_grad_()
+    with torch.no_grad():
+        call(**tensors, **rest)
+    with torch.inference_mode():
+        call(**tensors, **rest)
+    torch.cuda.synchronize()
+
+
+class _Norm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w):
+        y = torch.empty_like(x)
+        thl.rmsnorm(x, w, y, eps=1e-5)
+        ctx.save_for_backward(x, w)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w = ctx.saved_tensors
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        thl.rmsnorm_backward(x, dy, w, dx, dw, eps=1e-5)
+        return dx, dw
+
+
+@pytest.mark.gpu
+def test_inside_an_autograd_function():
+    # fp32 sums of 200 terms: each side within 1e-5 of the gradient's norm
+    g = torch.Generator().manual_seed(0)
+    x, w, up = torch.randn(30, 200, generator=g), 1 + 0.2 * torch.randn(200, generator=g), torch.randn(30, 200, generator=g)
+    X, W = x.double().requires_grad_(), w.double().requires_grad_()
+    ((X * torch.rsqrt(X.square().mean(dim=1, keepdim=True) + 1e-5) * W) * up.double()).sum().backward()
+    xd, wd = x.cuda().requires_grad_(), w.cuda().requires_grad_()
+    (_Norm.apply(xd, wd) * up.cuda()).sum().backward()
+    for got, want in ((xd.grad, X.grad), (wd.grad, W.grad)):
+        assert float((got.cpu().double() - want).norm()) <= 1e-5 * float(want.norm())
+
+
 # ------------------------------------------------------------------ out of memory
 
 @pytest.mark.gpu

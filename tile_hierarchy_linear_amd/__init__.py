@@ -375,7 +375,10 @@ def thl_gemm_w4(m, n, k, W, ldw, scales, X, ldx, C, ldc, D, ldd, alpha, beta, dt
 # current stream of the tensors' device, take their workspaces from torch on
 # that stream, and raise ValueError for a tensor of the wrong shape, type or
 # device, ThlError for what the library refuses and torch.OutOfMemoryError
-# where a workspace does not fit.  The tensors are read and checked in
+# where a workspace does not fit.  Autograd does not see them: a tensor that
+# requires a gradient raises ValueError where gradients are recorded (call them
+# under torch.no_grad() or inside a torch.autograd.Function, with the *_backward
+# forms as its backward).  The tensors are read and checked in
 # csrc/torch_ops.cpp: in Python that took as long as the launch.
 
 

@@ -15,6 +15,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <c10/core/Allocator.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -41,9 +42,16 @@ struct Refused : std::exception {
 };
 struct Raised : std::exception {};  // a Python error is set
 
+// Where autograd records (backward or forward mode), a call that it does not
+// see would be a constant to it, without a word.
 const at::Tensor& tensor(const char* what, PyObject* o) {
   if (!THPVariable_Check(o)) throw Refused("%s: a torch tensor is expected", what);
-  return THPVariable_Unpack(o);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  const c10::AutogradState& mode = c10::AutogradState::get_tls_state();
+  if ((mode.get_grad_mode() && t.requires_grad()) || (mode.get_fw_grad_mode() && t._fw_grad(0).defined()))
+    throw Refused("%s: requires a gradient, which these calls do not record; call them under torch.no_grad() or inside "
+                  "a torch.autograd.Function", what);
+  return t;
 }
 bool given(PyObject* o) { return o != Py_None; }
 
