@@ -122,6 +122,39 @@ def test_inside_an_autograd_function():
         assert float((got.cpu().double() - want).norm()) <= 1e-5 * float(want.norm())
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", FORMS)
+def test_outputs_count_as_written(form):
+    call, tensors, rest, written = _calls("cuda")[form]
+    before = {k: v._version for k, v in tensors.items()}
+    call(**tensors, **rest)
+    torch.cuda.synchronize()
+    for k, v in tensors.items():
+        assert (v._version > before[k]) == (k in written), k
+
+
+@pytest.mark.gpu
+def test_a_saved_tensor_that_is_overwritten_is_noticed():
+    p = torch.ones(4, 64, device="cuda", requires_grad=True)
+    h, x, w = torch.ones(4, 64, device="cuda"), torch.ones(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    loss = (p * h).sum()  # keeps h
+    thl.rmsnorm(x, w, torch.empty_like(x), residual=h, residual_out=h)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+@pytest.mark.gpu
+def test_inference_tensors():
+    with torch.inference_mode():
+        x, w, y = torch.ones(4, 64, device="cuda"), torch.ones(64, device="cuda"), torch.empty(4, 64, device="cuda")
+        thl.rmsnorm(x, w, y, eps=0.0)
+    assert bool((y == 1).all())
+    y2 = y.clone()
+    thl.rmsnorm(x, w, y, eps=0.0)  # and outside
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2)
+
+
 # ------------------------------------------------------------------ out of memory
 
 @pytest.mark.gpu

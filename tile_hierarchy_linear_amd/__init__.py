@@ -378,7 +378,7 @@ def thl_gemm_w4(m, n, k, W, ldw, scales, X, ldx, C, ldc, D, ldd, alpha, beta, dt
 # where a workspace does not fit.  Autograd does not see them: a tensor that
 # requires a gradient raises ValueError where gradients are recorded (call them
 # under torch.no_grad() or inside a torch.autograd.Function, with the *_backward
-# forms as its backward).  The tensors are read and checked in
+# forms as its backward), and outputs count as written in place.  The tensors are read and checked in
 # csrc/torch_ops.cpp: in Python that took as long as the launch.
 
 

@@ -401,12 +401,25 @@ void out_of_memory(const char* what) {
   Py_XDECREF(torch);
 }
 
-// One Python function: N positional arguments, errors as exceptions.
-template <thl_status (*F)(PyObject* const*), Py_ssize_t N>
+// An output was written: torch's own in-place operations count that, so that
+// autograd notices when a tensor that it keeps for a backward has changed.
+// (Inference tensors have no counter.)
+void written(PyObject* o) {
+  if (!given(o)) return;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
+// One Python function: N positional arguments, of which those at OUT are
+// outputs; errors as exceptions.
+template <thl_status (*F)(PyObject* const*), Py_ssize_t N, int... OUT>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   try {
     if (n != N) throw Refused("%d arguments are expected", static_cast<int>(N));
-    return PyLong_FromLong(F(args));
+    const thl_status status = F(args);
+    // (a HIP error may come behind a first launch)
+    if (status == THL_OK || status == THL_ERR_HIP) (written(args[OUT]), ...);
+    return PyLong_FromLong(status);
   } catch (const Raised&) {
     return nullptr;
   } catch (const Refused& e) {
@@ -421,19 +434,20 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return nullptr;
 }
 
-template <thl_status (*F)(PyObject* const*), Py_ssize_t N>
+template <thl_status (*F)(PyObject* const*), Py_ssize_t N, int... OUT>
 PyMethodDef method(const char* name) {
-  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<F, N>)), METH_FASTCALL, nullptr};
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<F, N, OUT...>)), METH_FASTCALL,
+          nullptr};
 }
 
 PyMethodDef methods[] = {
-    method<rmsnorm, 8>("rmsnorm"),
-    method<rmsnorm_backward, 7>("rmsnorm_backward"),
-    method<moe_sort, 5>("moe_sort"),
-    method<moe_gather, 6>("moe_gather"),
-    method<moe_combine, 4>("moe_combine"),
-    method<moe_combine_backward, 6>("moe_combine_backward"),
-    method<gemm_w4, 12>("gemm_w4"),
+    method<rmsnorm, 8, 2, 5, 7>("rmsnorm"),
+    method<rmsnorm_backward, 7, 3, 4>("rmsnorm_backward"),
+    method<moe_sort, 5, 2, 3, 4>("moe_sort"),
+    method<moe_gather, 6, 2, 4>("moe_gather"),
+    method<moe_combine, 4, 2>("moe_combine"),
+    method<moe_combine_backward, 6, 4, 5>("moe_combine_backward"),
+    method<gemm_w4, 12, 2>("gemm_w4"),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
