@@ -493,6 +493,12 @@ thl_status thl_moe_combine_backward(int64_t m, int64_t n, int64_t topk, const vo
  * The epilogue is thl_gemm's (sfd unused); D may be C exactly, any other
  * overlap with D is THL_ERR_INVALID.  Products are exact in fp32; the sum of
  * a group, its zero point and scale, and the sum over groups round in fp32.
+ * A group is summed before its scale, integer codes with an offset: (16 + q)
+ * X(p,j) less (16 + z) X(p,j) (q + 8 and 8 in their places for I4X2).  Over any
+ * 256 codes of a group the magnitudes |X(p,j)|, added and times 31 (or 16 + z,
+ * where that is more; 6 for E2M1X2), have to stay below fp32's largest value:
+ * past it the result may be an infinity or NaN though the formula's is finite.
+ * (F16 activations always stay below, BF16 ones up to 4e33 in magnitude.)
  * A token that holds an infinity or NaN gives an infinity or NaN wherever
  * integer codes meet it; other tokens do not see it.  k = 0 gives act(beta*C + bias).  Any n up
  * to 2^21, but every 64 tokens stream the weights once more: this call is for

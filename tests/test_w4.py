@@ -266,3 +266,44 @@ def test_subnormal_activations(type_w, group, x, n):
     torch.cuda.synchronize()
     want, _ = ref.gemm_w4(w, type_w, scales, group, zeros, xt.cuda(), k)
     assert torch.equal(d.double().cpu(), want.cpu() * up)
+
+
+@pytest.mark.parametrize("type_w", ["u4", "i4", "e2m1"])
+@pytest.mark.parametrize("n", [1, 2, 3, 20])
+def test_large_finite_activations(type_w, n):
+    """The largest activations that the sums before a group's scale leave finite: their magnitudes, times 31 (271 with
+    the largest zero point, 6 for E2M1), stay below 2^128.  One activation a token, of 2^123 (2^119, 2^125); the
+    products are exact, and so is a result that is small or zero."""
+    m, k = 48, 512
+    group = 32 if type_w == "e2m1" else 128
+    w, _, _, _ = _make(m, n, k, type_w, group)
+    for z, size in {"u4": ((15, 2.0 ** 123), (255, 2.0 ** 119)), "i4": ((0, 2.0 ** 123),),
+                    "e2m1": ((0, 2.0 ** 125),)}[type_w]:
+        zeros = torch.full((m, k // group), z, dtype=torch.uint8, device="cuda") if type_w == "u4" else None
+        scales = (torch.full((m, k // group), 117, dtype=torch.uint8, device="cuda") if type_w == "e2m1" else
+                  torch.full((m, k // group), 2.0 ** -10, dtype=torch.bfloat16, device="cuda"))
+        xt = torch.zeros(n, k, dtype=torch.bfloat16)
+        for t in range(n):
+            xt[t, (41 * t + 9) % k] = size * (1 if t % 2 else -1)
+        d = torch.empty(n, m, device="cuda")
+        thl.gemm_w4(w, xt.cuda(), d, scales=scales, group=group, type_w=type_w, zeros=zeros)
+        torch.cuda.synchronize()
+        want, _ = ref.gemm_w4(w, type_w, scales, group, zeros, xt, k)
+        assert torch.equal(d.double().cpu(), want)
+        assert type_w != "u4" or z != 15 or bool((want == 0).any())  # some code is the zero point
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 20])
+def test_activations_as_large_as_bf16_sums_allow(n):
+    # every activation at 4e33 and the largest zero point: 256 of them times 271 are finite, and so is every result
+    m, k, group = 40, 1024, 256
+    w, _, _, _ = _make(m, n, k, "u4", group)
+    zeros = torch.full((m, k // group), 255, dtype=torch.uint8, device="cuda")
+    scales = torch.full((m, k // group), 2.0 ** -4, dtype=torch.bfloat16, device="cuda")
+    xt = torch.full((n, k), 4e33, dtype=torch.bfloat16, device="cuda")
+    d = torch.empty(n, m, device="cuda")
+    thl.gemm_w4(w, xt, d, scales=scales, group=group, zeros=zeros)
+    torch.cuda.synchronize()
+    want, bound = ref.gemm_w4(w, "u4", scales, group, zeros, xt, k)
+    # the oracle's bound counts terms of up to 31 |x|; here the zero point's are up to 271 |x|
+    _check(d, want, bound * 271 / 31 + ref.half_step(want, torch.float32))
