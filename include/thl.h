@@ -376,6 +376,9 @@ thl_status thl_gemm_grouped(int64_t count, const thl_group_problem* problems,
  *          sfy[j*ld_sfy + b], ld_sfy >= ceil(m/32) (a product that reads them
  *          as sfa or sfb wants a multiple of 16), E2M1X2 with ldy even.
  *   eps    >= 0 and finite.  With eps = 0 a token of zeros is 0/0, NaN.
+ * The squares are added in fp32: a token whose sum of them passes fp32's range
+ * (features of 1e19, say) gives zeros, and with eps = 0 one whose squares are
+ * all below it infinities.
  * S may be X or R exactly (same pointer, leading dimension and type), and Y
  * may be X; any other overlap with an output is THL_ERR_INVALID.
  */

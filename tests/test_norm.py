@@ -358,3 +358,21 @@ def test_one_scale_keeps_nan():
     thl.rmsnorm(torch.ones(1, 64, device="cuda"), w, y, eps=0.0, scale=0.3)
     torch.cuda.synchronize()
     assert bool(torch.isnan(y[0, 5].float())) and not bool(torch.isnan(y.float()[0, torch.arange(64) != 5]).any())
+
+
+@pytest.mark.parametrize("m", [64, 1003, 17000])
+def test_range_of_the_squares(m):
+    # every feature +-2^e: sums of squares m 2^(2e), inside fp32's range up to e = 56 and past it from 64 on
+    sign = torch.where(torch.arange(m) % 3 == 0, -1.0, 1.0)
+    w, y = torch.ones(m, device="cuda"), torch.empty(1, m, device="cuda")
+    rel = ref.rmsnorm(torch.ones(1, m), None, torch.ones(m), 0.0)[2]
+    for e in (-56, -1, 0, 56):
+        thl.rmsnorm((sign * 2.0 ** e).cuda().reshape(1, m), w, y, eps=0.0)
+        torch.cuda.synchronize()
+        _check_float(y, sign.double().reshape(1, m), rel, e)
+    thl.rmsnorm((sign * 2.0 ** 64).cuda().reshape(1, m), w, y, eps=EPS)
+    torch.cuda.synchronize()
+    assert bool((y == 0).all())
+    thl.rmsnorm((sign * 2.0 ** -80).cuda().reshape(1, m), w, y, eps=0.0)
+    torch.cuda.synchronize()
+    assert bool(torch.isinf(y).all())
