@@ -376,3 +376,87 @@ def test_range_of_the_squares(m):
     thl.rmsnorm((sign * 2.0 ** -80).cuda().reshape(1, m), w, y, eps=0.0)
     torch.cuda.synchronize()
     assert bool(torch.isinf(y).all())
+
+
+def _plain64(x, r, w):
+    """(s, y) in fp64 on the GPU."""
+    s = x.double() if r is None else x.double() + r.double()
+    return s, s * torch.rsqrt(s.square().mean(dim=1, keepdim=True) + EPS) * w.double()
+
+
+def _near(got, want, bound):
+    return bool(((got.double() - want).abs() <= bound).all())
+
+
+# more tokens than workgroups (8,192 of four wavefronts, 2,048 of sixteen), for every width from 1,025 on, whole and ragged
+@pytest.mark.parametrize("n,m", [(1100, 4104), (1100, 6000), (1100, 6152), (1100, 8192), (8300, 1800), (8300, 2050),
+                                 (8300, 4096), (8300, 4099), (8300, 6144), (8300, 6147), (8300, 8192), (2100, 8195),
+                                 (2100, 16384), (2100, 16411)])
+@pytest.mark.parametrize("x,res,y", [("bf16", "bf16", "bf16"), ("f16", "f32", "f32")])
+def test_more_tokens_than_workgroups(n, m, x, res, y):
+    g = torch.Generator(device="cuda").manual_seed(m)
+    xt = torch.randn(n, m, generator=g, device="cuda").to(F[x])
+    rt = (3 * torch.randn(n, m, generator=g, device="cuda")).to(F[res])
+    wt = (1 + 0.3 * torch.randn(m, generator=g, device="cuda")).to(F[x])
+    st, yt = torch.full_like(rt, float("nan")), torch.full((n, m), float("nan"), dtype=F[y], device="cuda")
+    thl.rmsnorm(xt, wt, yt, eps=EPS, residual=rt, residual_out=st)
+    torch.cuda.synchronize()
+    rel = ref.rmsnorm(xt[:1], rt[:1], wt, EPS)[2]
+    for a in range(0, n, 1024):  # pieces of the fp64 form
+        c = slice(a, min(n, a + 1024))
+        s, want = _plain64(xt[c], rt[c], wt)
+        assert _near(st[c], s, ref.half_step(s, st.dtype) + ref.U * s.abs())
+        assert _near(yt[c], want, rel * want.abs() + ref.half_step(want, yt.dtype) * (1 + 2 * rel))
+
+
+# widths off eight: the last two runs of a row overlap, and every lane has to read before any stores
+@pytest.mark.parametrize("m", [9, 65, 777, 1025, 2049, 4099, 6147, 8195, 12001, 16411])
+@pytest.mark.parametrize("n", [5, 1100])
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+def test_ragged_rows_in_place(m, n, x):
+    g = torch.Generator(device="cuda").manual_seed(m)
+    xt = torch.randn(n, m, generator=g, device="cuda").to(F[x])
+    rt = (3 * torch.randn(n, m, generator=g, device="cuda")).to(F[x])
+    wt = (1 + 0.3 * torch.randn(m, generator=g, device="cuda")).to(F[x])
+    st, yt = torch.empty_like(xt), torch.empty_like(xt)
+    thl.rmsnorm(xt, wt, yt, eps=EPS, residual=rt, residual_out=st)
+    for over in ("s over r, y over x", "s over x", "y over x"):
+        x2, r2, s2, y2 = xt.clone(), rt.clone(), torch.empty_like(xt), torch.empty_like(xt)
+        s2 = r2 if over.startswith("s over r") else x2 if over == "s over x" else s2
+        y2 = x2 if "y over x" in over else y2
+        thl.rmsnorm(x2, wt, y2, eps=EPS, residual=r2, residual_out=s2)
+        torch.cuda.synchronize()
+        assert torch.equal(s2, st) and torch.equal(y2, yt), over
+
+
+@pytest.mark.parametrize("n,m", [(700, 2056), (600, 3001), (1300, 4096), (5000, 1024), (4500, 513), (4200, 2048),
+                                 (1100, 6000), (600, 12288)])
+@pytest.mark.parametrize("g", ["bf16", "f32"])
+def test_backward_sums_dw_over_tokens_of_a_workgroup(n, m, g):
+    _grad(n, m, s="f32" if g == "f32" else "bf16", g=g, seed=n)
+
+
+def test_longest_tokens():
+    # 2^26 features, the most that a call takes: sums, gradients and dw against fp64 on the GPU
+    m = 1 << 26
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(1, m, generator=g, device="cuda").bfloat16()
+    dy = torch.randn(1, m, generator=g, device="cuda").bfloat16()
+    w = (1 + 0.3 * torch.randn(m, generator=g, device="cuda")).bfloat16()
+    y, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty(m, device="cuda")
+    thl.rmsnorm(x, w, y, eps=EPS)
+    thl.rmsnorm_backward(x, dy, w, dx, dw, eps=EPS)
+    torch.cuda.synchronize()
+    X, G, W = x.double(), dy.double(), w.double()
+    rho = torch.rsqrt(X.square().mean(dim=1, keepdim=True) + EPS)
+    terms = 64 + m / 8192 + 22  # as the oracle counts them
+    rel = (terms / 2 + 8) * ref.U
+    want = X * rho * W
+    assert _near(y, want, rel * want.abs() + ref.half_step(want, y.dtype) * (1 + 2 * rel))
+    h, t = rho * X, W * G
+    want = rho * (t - h * (t * h).mean(dim=1, keepdim=True))
+    c = 3 * (terms + 8) * ref.U
+    bound = c * rho * (t.abs() + h.abs() * (t * h).abs().mean(dim=1, keepdim=True))
+    assert _near(dx, want, bound + ref.half_step(want, dx.dtype) * 1.001)
+    want = (G * h)[0]
+    assert _near(dw, want, (rel + 4 * ref.U) * want.abs() + ref.half_step(want, dw.dtype))
