@@ -294,3 +294,83 @@ def test_gather_of_the_longest_token():
     y = torch.zeros(2, m, device="cuda")
     thl.moe_gather(x, torch.tensor([[1]], dtype=torch.int32, device="cuda"), y)
     assert torch.equal(y[1:].view(torch.int32), x.view(torch.int32)) and not bool(y[0].any())
+
+
+# rows of packed codes: bytes a row of m elements, and elements a unit of whole bytes
+PACKED = {"e2m1": (lambda m: (m + 1) // 2, 2, 1), "i4": (lambda m: (m + 1) // 2, 2, 1),
+          "u4": (lambda m: (m + 1) // 2, 2, 1), "e2m3": (lambda m: (6 * m + 7) // 8, 4, 3),
+          "e3m2": (lambda m: (6 * m + 7) // 8, 4, 3), "i8": (lambda m: m, 1, 1), "i32": (lambda m: 4 * m, 1, 4),
+          "e8m0": (lambda m: m, 1, 1)}
+
+
+@pytest.mark.parametrize("fmt", sorted(PACKED))
+@pytest.mark.parametrize("m", [1, 5, 31, 33, 100, 1001, 4096])
+def test_gather_of_packed_rows(fmt, m):
+    size, per, unit = PACKED[fmt]
+    n, topk, experts = 21, 3, 5
+    rows, _, _ = _sort(_ids(n, topk, experts, seed=m, lo=-1), experts)
+    whole = -(-m // per) + 2  # units of whole bytes a row, two of them padding
+    g = torch.Generator().manual_seed(m)
+    x = torch.randint(0, 256, (n, whole * unit), generator=g).to(torch.uint8).cuda()
+    y = torch.full((n * topk, whole * unit), 0xEE, dtype=torch.uint8, device="cuda")
+    nb = (m + 31) // 32
+    sfx = torch.randint(0, 256, (n, nb + 1), generator=g).to(torch.uint8).cuda()
+    sfy = torch.full((n * topk, nb + 2), 0xEE, dtype=torch.uint8, device="cuda")
+    st = thl.thl_moe_gather(m, n, topk, x.data_ptr(), whole * per, sfx.data_ptr(), nb + 1, rows.data_ptr(), n * topk,
+                            y.data_ptr(), whole * per, sfy.data_ptr(), nb + 2, fmt,
+                            torch.cuda.current_stream().cuda_stream)
+    assert st == thl.THL_OK
+    torch.cuda.synchronize()
+    want, want_sf = torch.full_like(y, 0xEE).cpu(), torch.full_like(sfy, 0xEE).cpu()
+    for j, places in enumerate(rows.cpu().tolist()):
+        for p in places:
+            if p >= 0:
+                want[p, :size(m)] = x[j, :size(m)].cpu()
+                want_sf[p, :nb] = sfx[j, :nb].cpu()
+    assert torch.equal(y.cpu(), want) and torch.equal(sfy.cpu(), want_sf)
+
+
+def test_sort_of_the_most_choices():
+    # 2^30: places and their inverse, the experts in order, and within one the choices in order
+    n, topk, experts = 1 << 27, 8, 100
+    g = torch.Generator(device="cuda").manual_seed(2)
+    ids = torch.empty(n, topk, dtype=torch.int32, device="cuda")
+    ids.random_(0, experts + 1, generator=g)  # `experts` itself is dropped
+    rows, offsets = torch.empty_like(ids), torch.empty(experts + 1, dtype=torch.int32, device="cuda")
+    order = torch.full((n * topk,), -7, dtype=torch.int32, device="cuda")
+    thl.moe_sort(ids, experts, rows, offsets, order=order)
+    torch.cuda.synchronize()
+    ids, rows = ids.view(-1), rows.view(-1)
+    counts = torch.zeros(experts, dtype=torch.int64, device="cuda")
+    step, last = 1 << 26, -1
+    for a in range(0, n * topk, step):
+        counts += torch.stack([(ids[a:a + step] == e).sum() for e in range(experts)])
+    assert offsets.tolist() == [0] + counts.cumsum(0).tolist()
+    kept = int(offsets[-1])
+    assert kept < n * topk and bool((order[kept:] == -7).all())
+    for a in range(0, kept, step):
+        at = order[a:min(kept, a + step)].long()
+        assert bool((rows[at] == torch.arange(a, a + at.numel(), device="cuda")).all())
+        key = (ids[at].long() << 32) | at
+        assert int(key[0]) > last and bool((key[1:] > key[:-1]).all())
+        last = int(key[-1])
+    for a in range(0, n * topk, step):
+        assert bool(((rows[a:a + step] == -1) == (ids[a:a + step] == experts)).all())
+
+
+def test_combine_of_the_longest_tokens():
+    m = 1 << 26
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randint(-3, 4, (3, m), generator=g, device="cuda").bfloat16()
+    rows = torch.tensor([[2, 0]], dtype=torch.int32, device="cuda")
+    weights = torch.tensor([[2.0, -0.5]], device="cuda")
+    y, dx, dw = torch.empty(1, m, device="cuda"), torch.full_like(x, 9.0), torch.empty_like(weights)
+    thl.moe_combine(x, rows, y, weights=weights)
+    torch.cuda.synchronize()
+    assert torch.equal(y[0], 2 * x[2].float() - 0.5 * x[0].float())
+    dy = torch.randint(0, 2, (1, m), generator=g, device="cuda").bfloat16()
+    thl.moe_combine_backward(dy, x, rows, weights, dx, dw)
+    torch.cuda.synchronize()
+    assert torch.equal(dx[2], 2 * dy[0]) and torch.equal(dx[0], -0.5 * dy[0]) and bool((dx[1] == 9.0).all())
+    # whole numbers, of which 256 lanes add 2^18 each: exact
+    assert torch.equal(dw.double()[0], torch.stack([(dy.double()[0] * x[r].double()).sum() for r in (2, 0)]))
