@@ -307,3 +307,65 @@ def test_activations_as_large_as_bf16_sums_allow(n):
     want, bound = ref.gemm_w4(w, "u4", scales, group, zeros, xt, k)
     # the oracle's bound counts terms of up to 31 |x|; here the zero point's are up to 271 |x|
     _check(d, want, bound * 271 / 31 + ref.half_step(want, torch.float32))
+
+
+def _exact(m, n, k, type_w, group, x, seed=0):
+    """Small whole activations, scales that are powers of two: every product and sum is a multiple of 1/8 (a scale of
+    1/4 times a step of 1/2) below 2^20, so exact in fp32, in any order."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    groups = -(-k // group)
+    assert k * 3 * (31 + 15) < 2 ** 22  # |x| <= 3 times 16 + q and 16 + z, in steps of 1/4
+    w = torch.randint(0, 256, (m, (k + 1) // 2), generator=g, device="cuda").to(torch.uint8)
+    xt = torch.randint(-3, 4, (n, k), generator=g, device="cuda").to(F[x])
+    e = torch.randint(-2, 1, (m, groups), generator=g, device="cuda")
+    zeros = torch.randint(0, 16, (m, groups), generator=g, device="cuda").to(torch.uint8) if type_w == "u4" else None
+    scales = (127 + e).to(torch.uint8) if type_w == "e2m1" else torch.pow(2.0, e.float()).to(F[x])
+    d = torch.full((n, m), float("nan"), device="cuda")
+    thl.gemm_w4(w, xt, d, scales=scales, group=group, type_w=type_w, zeros=zeros)
+    torch.cuda.synchronize()
+    values = torch.tensor(ref.E2M1 + [-v for v in ref.E2M1] if type_w == "e2m1" else
+                          [float(q if q < 8 or type_w == "u4" else q - 16) for q in range(16)], dtype=torch.float64,
+                          device="cuda")
+    x64 = xt.double().t().contiguous()
+    at = (torch.arange(k, device="cuda") // group)
+    for a in range(0, m, 4096):  # pieces of the fp64 form
+        c = slice(a, min(m, a + 4096))
+        v = values[torch.stack([w[c] & 15, w[c] >> 4], dim=2).reshape(w[c].shape[0], -1)[:, :k].int()]
+        if zeros is not None:
+            v -= zeros[c].double()[:, at]
+        v *= torch.pow(2.0, e[c].double())[:, at]
+        want = (v @ x64).t()
+        assert torch.equal(d[:, c].double(), want), (a, int((d[:, c].double() != want).sum()))
+
+
+# one and two tokens: K over 1 to 8 wavefronts, several slices each, a part of a piece at its end, and several
+# blocks of rows a workgroup
+@pytest.mark.parametrize("m,k", [(40000, 1536), (4200, 2048), (4200, 4096), (4200, 6144), (28672, 8192), (4200, 10240),
+                                 (4200, 12288), (4200, 14336), (9000, 16384), (9000, 20493), (4200, 27000)])
+@pytest.mark.parametrize("type_w,group", [("u4", 128), ("i4", 64), ("e2m1", 32), ("u4", 1 << 20)])
+def test_down_the_rows(m, k, type_w, group):
+    for n in (1, 2):
+        _exact(m, n, k, type_w, group, "bf16" if n == 1 else "f16", seed=k)
+
+
+# more tokens: so many features that K is not split, and a workgroup goes through sixteen units and a part of one
+@pytest.mark.parametrize("type_w,group", [("u4", 32), ("u4", 64), ("u4", 128), ("u4", 256), ("u4", 1 << 20), ("i4", 32),
+                                          ("i4", 64), ("i4", 128), ("i4", 1024), ("e2m1", 32)])
+@pytest.mark.parametrize("n", [3, 12, 20, 40, 64, 100])
+def test_along_k(type_w, group, n):
+    _exact(33000, n, 4166, type_w, group, "bf16", seed=n)
+    _exact(28672, n, 4096, type_w, group, "f16", seed=n)
+
+
+# and so few that it is split, with several sets of units a workgroup
+@pytest.mark.parametrize("type_w,group", [("u4", 128), ("i4", 32), ("e2m1", 32)])
+@pytest.mark.parametrize("n", [8, 24, 48, 64])
+def test_along_split_k(type_w, group, n):
+    assert thl.thl_gemm_w4_workspace(8192, n, 8192) > 0
+    _exact(8192, n, 8192, type_w, group, "bf16", seed=n)
+    _exact(5000, n, 20493, type_w, group, "f16", seed=n)
+
+
+@pytest.mark.parametrize("m,n,k", [(1 << 26, 1, 32), (1 << 26, 3, 40), (130, 1 << 21, 70)])
+def test_most_features_and_most_tokens(m, n, k):
+    _exact(m, n, k, "i4", 32, "bf16", seed=n)
