@@ -358,8 +358,9 @@ thl_status thl_gemm_grouped(int64_t count, const thl_group_problem* problems,
  * nothing and hold no state of their own: workspaces are the caller's, calls
  * that may overlap in time need one each, and every call can be captured into
  * a graph.  Results do not depend on timing.  Arrays are aligned to their
- * elements (THL_ERR_MISALIGNED otherwise; 8- and 4-bit arrays anywhere); m
- * above 2^26 and other sizes above INT32_MAX are THL_ERR_UNSUPPORTED.
+ * elements (THL_ERR_MISALIGNED otherwise; 8- and 4-bit arrays and the rows that
+ * thl_moe_gather copies lie anywhere); m above 2^26 and other sizes above
+ * INT32_MAX are THL_ERR_UNSUPPORTED.
  *
  * thl_rmsnorm -- the root-mean-square norm of each token, the residual added
  * before it:
@@ -419,7 +420,11 @@ thl_status thl_rmsnorm_backward(int64_t m, int64_t n, const void* S, int64_t lds
 /*
  * Tokens sorted by expert and back: the operands and results of a grouped
  * product whose problems are a layer's experts (problem e: the rows
- * offsets[e] .. offsets[e+1]-1 of the gathered array).
+ * offsets[e] .. offsets[e+1]-1 of the gathered array).  thl_gemm_grouped takes
+ * its problems' sizes and addresses on the host, so between the sort and the
+ * product the caller copies `offsets` there and waits for them: each of these
+ * calls can be captured into a graph, a layer with the product in it only
+ * where the sizes are known beforehand.
  *
  * thl_moe_sort -- the stable order of n tokens' topk choices by expert.
  *   ids      ids[j*ld_ids + t], token j's choice t: int32 (ids_bytes = 4) or
@@ -442,7 +447,9 @@ thl_status thl_moe_sort(int64_t n, int64_t topk, int64_t experts, const void* id
 
 /*
  * thl_moe_gather -- Y(:, rows[j*topk + t]) = X(:, j) for every choice that has
- * a place in 0 .. rows_y-1; other columns of Y are left as they were.  Any
+ * a place in 0 .. rows_y-1; other columns of Y are left as they were.  Places
+ * must differ (thl_moe_sort's do): a column that two tokens have may end up as
+ * a mixture of both.  Any
  * format of thl_dtype, copied bit for bit; with sfx and sfy (both or neither)
  * the ceil(m/32) E8M0 bytes of each token's blocks go along.  For E2M1X2,
  * I4X2 and U4X2 leading dimensions are even, for E2M3 and E3M2 multiples of

@@ -420,15 +420,17 @@ def rmsnorm_backward(s, dy, w, dx, dw=None, *, eps=1e-6, dres=None):
 
 def moe_sort(ids, experts, rows, offsets, *, order=None):
     """The stable order of (tokens, choices) int32 or int64 expert ids: each choice's row (int32, -1 when its id is
-    outside 0 .. experts-1), each expert's first row (experts + 1 of them), and each row's flat choice."""
+    outside 0 .. experts-1), each expert's first row (experts + 1 of them), and each row's flat choice.  A grouped
+    product over the experts takes the offsets on the host (offsets.tolist() waits for them)."""
     status = _ops.moe_sort(ids, experts, rows, offsets, order)
     if status:
         raise ThlError(status, "thl_moe_sort")
 
 
 def moe_gather(x, rows, y, *, sf=None, sf_y=None, type_x=None):
-    """y[rows[j, t]] = x[j], bit for bit, with the rows of block scales sf likewise into sf_y.  type_x: "e2m1" (two
-    codes a byte of a uint8 tensor) where the tensor's type does not say it.  Returns y."""
+    """y[rows[j, t]] = x[j], bit for bit, with the rows of block scales sf likewise into sf_y.  type_x: "e2m1", "i4" or
+    "u4" (two codes a byte), "e4m3", "e5m2" or "i8" where a one-byte tensor's type does not say it; fp6 rows go through
+    thl_moe_gather.  Returns y."""
     status = _ops.moe_gather(x, rows, y, sf, sf_y, type_x)
     if status:
         raise ThlError(status, "thl_moe_gather")

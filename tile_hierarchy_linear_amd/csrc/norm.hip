@@ -258,9 +258,10 @@ __global__ void __launch_bounds__(WPR * tokens_at_once(WPR) * 64) rmsnorm_grad_k
   if constexpr (CH > 0) {
     RawAny wr[NC];
     // dw's sums: of one run a lane in registers, of two in LDS, and the weights
-    // in fp32 in registers instead (4,096 tokens of 8,192 bf16 features: 47 us;
-    // 63 with one run a lane on twice the wavefronts; 2,048 of 16,384: 54 us,
-    // 100 with everything in registers, of which 30 spill)
+    // in fp32 in registers instead (with dr, and with the second launch: 4,096
+    // tokens of 8,192 bf16 features 52 us, 63 with one run a lane on twice the
+    // wavefronts; 2,048 of 16,384 58 us, 108 with everything in registers, of
+    // which 30 spill)
     constexpr bool IN_LDS = NC > 1;
     float acc[IN_LDS ? 1 : NC][8] = {};
     __shared__ __attribute__((aligned(16))) v4f held[IN_LDS ? 2 * NC * T : 1];
@@ -472,7 +473,8 @@ hipError_t launch_norm(NormArgs& a, hipStream_t st) {
 // 16,384 tokens of 1,024 bf16 features take 33.8 us with 2,048 rows on two
 // wavefronts each and 41.5 with 1,024 rows on four.  From 8,193 to 16,384 a
 // workgroup fills a compute unit, and 256 are all that run at a time: 2,048
-// tokens of 16,384 features take 61 us and 70 with 512 rows.
+// tokens of 16,384 features (both launches, with dr) take 58 us and 66 with 512
+// rows, of 12,288 features 48 and 53.
 int64_t grad_rows(int64_t m, int64_t n) {
   const int64_t tokens = m <= 512 ? (n + tokens_at_once(1) - 1) / tokens_at_once(1) : n;
   int64_t most = 512;
