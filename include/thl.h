@@ -418,6 +418,52 @@ thl_status thl_rmsnorm_backward(int64_t m, int64_t n, const void* S, int64_t lds
                                 struct ihipStream_t* stream);
 
 /*
+ * thl_layernorm -- the layer norm of each token, the residual added before it:
+ *   s = x + r,   h = (s - mean(s)) / sqrt(mean((s - mean(s))^2) + eps),   y_i = q(h_i * w_i + b_i)
+ * thl_rmsnorm's types, outputs and rules, and its roundings: fp32 throughout,
+ * the mean first and then the squares of the differences from it; S and Y
+ * round once.  W = NULL: ones.  B = NULL: zeros.  types->w is W's and B's.
+ * With eps = 0 a token of equal features is 0/0, NaN.
+ *
+ * thl_layernorm_backward -- its gradient (straight through Y's rounding): with
+ * rho = 1/sqrt(mean((s - mean(s))^2) + eps), h = rho * (s - mean(s)), t = w*dy,
+ *   dx = rho * (t - mean(t) - h * mean(t*h)) + dr
+ *   dw = sum over tokens of dy*h,   db = sum over tokens of dy.
+ * thl_rmsnorm_backward's rules; DW and DB may each be NULL (not wanted), are of
+ * types->dw (F32, or W's type where W is given) and are written, not added to.
+ *   workspace  thl_layernorm_backward_workspace(m, n) bytes, 4-byte aligned,
+ *              when DW or DB is wanted.
+ */
+thl_status thl_layernorm(int64_t m, int64_t n, const void* X, int64_t ldx, const void* R, int64_t ldr, void* S,
+                         int64_t lds, const void* W, const void* B, float eps, float y_scale, void* Y, int64_t ldy,
+                         uint8_t* sfy, int64_t ld_sfy, const thl_norm_types* types, struct ihipStream_t* stream);
+size_t thl_layernorm_backward_workspace(int64_t m, int64_t n);
+thl_status thl_layernorm_backward(int64_t m, int64_t n, const void* S, int64_t lds, const void* DY, int64_t lddy,
+                                  const void* DR, int64_t lddr, const void* W, float eps, void* DX, int64_t lddx,
+                                  void* DW, void* DB, void* workspace, size_t workspace_bytes,
+                                  const thl_norm_grad_types* types, struct ihipStream_t* stream);
+
+/*
+ * thl_mx_quantize -- an array as MX blocks, in either direction or in both with
+ * one read:
+ *   Y, sfy    blocks of 32 consecutive features of each token: Y(i,j) at
+ *             Y[i + j*ldy], SFY(b, j) for features 32b .. at sfy[j*ld_sfy + b]
+ *   YT, sfyt  blocks of 32 consecutive tokens of each feature, the transposed
+ *             array: YT(j,i) at YT[j + i*ldyt], SFYT(b, i) for tokens 32b .. at
+ *             sfyt[i*ld_sfyt + b] (what a weight's gradient multiplies)
+ * Y and sfy, YT and sfyt go together; one pair may be NULL.  X in F32, F16 or
+ * BF16; type_y E2M1X2 (ldy and ldyt even; in a row's last byte the missing odd
+ * element is zero), E4M3 or E5M2, by thl_gemm's MX-output rule.  A product that
+ * reads the scales as sfa or sfb wants leading dimensions of a multiple of 16.
+ * A block that holds a NaN has scale 255 (NaN) and elements of zero; an infinity
+ * is clamped like any magnitude, under a scale that makes it one in fp32 again.
+ * No output may overlap another array.
+ */
+thl_status thl_mx_quantize(int64_t m, int64_t n, const void* X, int64_t ldx, void* Y, int64_t ldy, uint8_t* sfy,
+                           int64_t ld_sfy, void* YT, int64_t ldyt, uint8_t* sfyt, int64_t ld_sfyt, thl_dtype type_x,
+                           thl_dtype type_y, struct ihipStream_t* stream);
+
+/*
  * Tokens sorted by expert and back: the operands and results of a grouped
  * product whose problems are a layer's experts (problem e: the rows
  * offsets[e] .. offsets[e+1]-1 of the gathered array).  thl_gemm_grouped takes
@@ -532,6 +578,86 @@ thl_status thl_gemm_w4(int64_t m, int64_t n, int64_t k, const void* W, int64_t l
                        const void* X, int64_t ldx, const void* C, int64_t ldc, void* D, int64_t ldd, float alpha,
                        float beta, const thl_dtypes* dtypes, const thl_epilogue* epilogue, void* workspace,
                        size_t workspace_bytes, struct ihipStream_t* stream);
+
+/*
+ * thl_moe_route -- each token's topk experts, from its logits L(:, j), and their
+ * weights:
+ *   p = softmax(l) or sigmoid(l);  the experts of the largest p + bias, in that
+ *   order, ties to the lowest;  w_t = scale * p_t, or with renormalize
+ *   scale * p_t / (sum of the chosen p), 0 where that sum is 0
+ *   ids, weights  ids[j*topk + t] (int32), weights[j*topk + t]: thl_moe_sort's,
+ *                 thl_moe_combine's and thl_moe_layer's.  A logit of -infinity or
+ *                 NaN masks its expert, which then adds nothing to the softmax's
+ *                 sum either; choices past the experts left get id -1, weight 0.
+ *   bias          experts values for the choice alone (may be NULL)
+ * Computed in fp32.  Without a bias the logits themselves are compared.  A logit
+ * of +infinity makes the softmax's weights NaN.  L in F32, F16 or BF16;
+ * experts <= 1024, topk <= 64 (THL_ERR_UNSUPPORTED above).  No output may
+ * overlap another array.
+ *
+ * thl_moe_route_backward -- the gradient of the weights with respect to the
+ * logits, the choice held fixed; DL of L's type, every element written.  ids as
+ * thl_moe_route left them; one outside 0 .. experts-1 has no gradient, one that
+ * a token has twice has the sum of both.  DL may be L exactly.
+ */
+enum { THL_ROUTE_SOFTMAX = 0, THL_ROUTE_SIGMOID = 1 };
+typedef struct {
+  thl_dtype type;  /* of the logits */
+  int score;       /* THL_ROUTE_* */
+  int renormalize; /* 0 or 1 */
+  float scale;     /* finite */
+} thl_route;
+
+thl_status thl_moe_route(int64_t n, int64_t topk, int64_t experts, const void* L, int64_t ldl, const float* bias,
+                         const thl_route* how, int32_t* ids, float* weights, struct ihipStream_t* stream);
+thl_status thl_moe_route_backward(int64_t n, int64_t topk, int64_t experts, const void* L, int64_t ldl,
+                                  const thl_route* how, const int32_t* ids, const float* dweights, void* DL,
+                                  int64_t lddl, struct ihipStream_t* stream);
+
+/*
+ * thl_moe_layer -- a layer of experts for a few tokens, its products included:
+ *   u_t = act(W1g x + b1g) * (W1u x + b1u)   (THL_MOE_GATED)   or   act(W1 x + b1)
+ *   Y(:, j) = sum over t of weights[j*topk + t] * (W2 u_t + b2)
+ * with x = X(:, j) and the matrices of expert ids[j*ld_ids + t] (int32 or int64
+ * by ids_bytes).  An id outside 0 .. experts-1 adds nothing, whatever its
+ * weight; a token without any gets zeros.  Nothing passes through the host, so
+ * the whole layer can be captured into a graph.
+ *   matrices  up: hidden rows of m values, or with THL_MOE_GATED 2 * hidden, the
+ *             gates' rows first; down: m rows of hidden values.  Row i of expert
+ *             e starts at w[e*stride + i*ld] (elements), K contiguous, as the
+ *             products' A with opA = T.  type: X's (F16 or BF16), or E4M3 or
+ *             E2M1X2 with E8M0 scales (MX: SF(i,b) of expert e at
+ *             sf[e*stride_sf + i*ld_sf + b], ld_sf >= ceil(k/32); E2M1X2 with ld
+ *             and stride even).  bias (may be NULL): of each expert's rows, at
+ *             bias[e*stride_bias + i], F32, F16 or BF16.
+ *   flags     THL_MOE_GATED and at most one of THL_MOE_RELU, THL_MOE_GELU (the
+ *             erf form) and THL_MOE_SILU
+ *   types     X F16 or BF16; Y F32, F16 or BF16
+ * Sums are fp32; u is kept with 16 significant bits (magnitudes above bf16's
+ * largest, 3.39e38, count as infinite); Y rounds once.  A token that holds an
+ * infinity or NaN gives infinities or NaN; other tokens do not see it.
+ * n * topk <= 1024 (THL_ERR_UNSUPPORTED above): every 16 choices of an expert
+ * stream its weights once more.
+ *   workspace  thl_moe_layer_workspace(m, hidden, n, topk) bytes, 4-byte aligned;
+ *              not read before it is written, overlapping nothing.
+ */
+enum { THL_MOE_GATED = 1, THL_MOE_RELU = 2, THL_MOE_GELU = 4, THL_MOE_SILU = 8 };
+typedef struct {
+  const void* w;
+  int64_t ld, stride;
+  const uint8_t* sf;
+  int64_t ld_sf, stride_sf;
+  const void* bias;
+  int64_t stride_bias;
+  thl_dtype type, type_bias;
+} thl_expert_matrix;
+
+size_t thl_moe_layer_workspace(int64_t m, int64_t hidden, int64_t n, int64_t topk);
+thl_status thl_moe_layer(int64_t m, int64_t hidden, int64_t n, int64_t topk, int64_t experts, const void* X,
+                         int64_t ldx, const void* ids, int64_t ld_ids, int ids_bytes, const float* weights,
+                         const thl_expert_matrix* up, const thl_expert_matrix* down, unsigned flags, void* Y,
+                         int64_t ldy, thl_dtype type_x, thl_dtype type_y, void* workspace, size_t workspace_bytes,
+                         struct ihipStream_t* stream);
 
 /* Static text for a status code. */
 const char* thl_status_string(int status);

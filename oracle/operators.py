@@ -145,3 +145,160 @@ def gemm_w4(codes, type_w, scales, group, zeros, x, k):
         pieces = -(-(cut.stop - cut.start) // 256)
         b += size * (2 * (length + 4) * 2 * U * (31.0 if type_w != "e2m1" else 6.0) + (groups * pieces + 8 + 4) * U * 31.0)
     return y, b
+
+
+def _terms(m):
+    """Additions that a term of a sum over m features takes part in (as counted in rmsnorm)."""
+    return 64 + m / 8192 + 6 + 16
+
+
+def layernorm(x, r, w, b, eps):
+    """(s, y, bound of y before its rounding).  The mean is off by its sum's additions, and every difference from it
+    by that and the rounding of s; the squares of the differences sum to the variance, in which a shift of all
+    differences counts squared only, as they sum to zero."""
+    s = f64(x) if r is None else f64(x) + f64(r)
+    m = s.shape[1]
+    d = s - s.mean(dim=1, keepdim=True)
+    rho = 1.0 / torch.sqrt((d * d).mean(dim=1, keepdim=True) + eps)
+    h, e_h = _centred(s, d, rho, m)
+    W = torch.ones(m, dtype=torch.float64) if w is None else f64(w)
+    B = torch.zeros(m, dtype=torch.float64) if b is None else f64(b)
+    y = h * W + B
+    return s, y, W.abs() * e_h + 3 * U * ((h * W).abs() + B.abs())
+
+
+def _centred(s, d, rho, m):
+    """The normalised features and their bound."""
+    shift = (_terms(m) + 3) * U * s.abs().mean(dim=1, keepdim=True)
+    rel = (_terms(m) / 2 + 8) * U + (rho * shift) ** 2 + rho * rho * U * (d * s).abs().mean(dim=1, keepdim=True)
+    h = d * rho
+    return h, rho * (shift + 2 * U * s.abs()) + h.abs() * rel
+
+
+def layernorm_backward(s, dy, w, dr, eps):
+    """(dx, dw, db, and their bounds) of the fp32 kernel, before the outputs' roundings."""
+    s, dy = f64(s), f64(dy)
+    n, m = s.shape
+    W = torch.ones(m, dtype=torch.float64) if w is None else f64(w)
+    d = s - s.mean(dim=1, keepdim=True)
+    rho = 1.0 / torch.sqrt((d * d).mean(dim=1, keepdim=True) + eps)
+    h, e_h = _centred(s, d, rho, m)
+    t = W * dy
+    level, along = t.mean(dim=1, keepdim=True), (t * h).mean(dim=1, keepdim=True)
+    c = (_terms(m) + 4) * U
+    e_along = c * (t * h).abs().mean(dim=1, keepdim=True) + (t.abs() * e_h).mean(dim=1, keepdim=True)
+    part = t - level - h * along
+    # rho is off by its share of h's bound: a relative e_h / |h| at most terms / 2 + 8 roundings and the shifts'
+    shift = (_terms(m) + 3) * U * s.abs().mean(dim=1, keepdim=True)
+    rel = (_terms(m) / 2 + 8) * U + (rho * shift) ** 2 + rho * rho * U * (d * s).abs().mean(dim=1, keepdim=True)
+    bx = rho * (4 * U * (t.abs() + level.abs() + (h * along).abs()) + c * t.abs().mean(dim=1, keepdim=True)
+                + h.abs() * e_along + e_h * along.abs() + rel * part.abs())
+    dx = rho * part
+    if dr is not None:
+        dx = dx + f64(dr)
+        bx = bx + U * (f64(dr).abs() + dx.abs())
+    steps = (n + 64 + 64) * U  # as in rmsnorm_backward
+    bw = steps * (dy * h).abs().sum(dim=0) + (dy.abs() * (e_h + U * h.abs())).sum(dim=0)
+    return dx, (dy * h).sum(dim=0), dy.sum(dim=0), bx, bw, steps * dy.abs().sum(dim=0)
+
+
+def mx_quantize(x, kind):
+    """(elements (n, m) as fp64 values before the block scale, scale codes (n, blocks)) of an (n, m) array: exact.  A
+    block with a NaN: scale 255, elements of zero."""
+    v = f64(x)
+    n, m = v.shape
+    nb = -(-m // 32)
+    b = torch.nn.functional.pad(v, (0, 32 * nb - m)).reshape(n, nb, 32)
+    bad = torch.isnan(b).any(dim=2)
+    b = torch.where(bad[:, :, None], 0.0, b)
+    amax = b.abs().amax(dim=2)
+    finite = torch.where(torch.isinf(amax), 2.0 ** 128, amax)
+    e = (torch.frexp(finite).exponent.double() - 1 - EMAX[kind]).clamp(-127, 127)
+    code = torch.where(amax > 0, e + 127, 0.0)
+    q = (b / torch.pow(2.0, code - 127)[:, :, None]).clamp(-TOP[kind], TOP[kind])
+    a = q.abs()
+    low = torch.floor(torch.log2(a.clamp(min=2.0 ** EMIN[kind])))
+    low = torch.where(torch.pow(2.0, low) > a.clamp(min=2.0 ** EMIN[kind]), low - 1, low)  # (log2 next to a power)
+    step = torch.pow(2.0, low - MANT[kind])
+    r = torch.round(a / step) * step  # half to even
+    r = torch.copysign(r.clamp(max=TOP[kind]), q)
+    return r.reshape(n, 32 * nb)[:, :m], torch.where(bad, 255.0, code).to(torch.uint8)
+
+
+def moe_route(logits, topk, score, renorm, scale, bias=None):
+    """(ids, weights, p, values that were compared), plain loops."""
+    l = f64(logits)
+    n, experts = l.shape
+    live = l > -torch.inf  # False for NaN
+    top = torch.where(live, l, -torch.inf).amax(dim=1, keepdim=True)
+    p = torch.where(live, torch.exp(l - torch.where(live.any(dim=1, keepdim=True), top, 0.0)), 0.0)
+    if score == "softmax":
+        p = p / p.sum(dim=1, keepdim=True).clamp(min=1e-300)  # (a row of masks alone: zeros)
+    else:
+        p = torch.where(live, torch.sigmoid(l), 0.0)
+    by = torch.where(live, l if bias is None else p + f64(bias), -torch.inf)
+    ids = torch.full((n, topk), -1, dtype=torch.int32)
+    for j in range(n):
+        order = sorted((e for e in range(experts) if by[j, e] > -torch.inf), key=lambda e: (-float(by[j, e]), e))
+        for t, e in enumerate(order[:topk]):
+            ids[j, t] = e
+    chosen = torch.where(ids >= 0, p.gather(1, ids.long().clamp(min=0)), 0.0)
+    total = chosen.sum(dim=1, keepdim=True) if renorm else torch.ones(n, 1, dtype=torch.float64)
+    return ids, torch.where(total > 0, scale * chosen / total, 0.0), p, by
+
+
+def moe_route_backward(logits, ids, dweights, score, renorm, scale):
+    """dlogits by autograd in fp64."""
+    l = f64(logits).requires_grad_()
+    live = l.detach() > -torch.inf
+    with torch.enable_grad():
+        if score == "softmax":
+            p = torch.softmax(torch.where(live, l, -1e300), dim=1)
+        else:
+            p = torch.where(live, torch.sigmoid(l), 0.0)
+        ok = (ids >= 0) & (ids < l.shape[1])
+        at = torch.where(ok, ids, 0).long()
+        w = torch.where(ok, p.gather(1, at), 0.0)
+        if renorm:
+            w = w / w.sum(dim=1, keepdim=True).clamp(min=1e-300)
+        (scale * w * f64(dweights)).sum().backward()
+    return l.grad
+
+
+def moe_layer(x, ids, weights, w1, w2, gated, act, b1=None, b2=None):
+    """(y, bound before y's rounding) for matrices of fp64 values (experts, rows, k).  Sums of K products are counted at
+    K + 8 whole steps of fp32, activations at a slope of 1.13 and four roundings, u's planes at 2^-16."""
+    x, wt = f64(x), f64(weights)
+    n, m = x.shape
+    experts, hidden = w1.shape[0], w2.shape[2]
+    y, b = torch.zeros(n, m, dtype=torch.float64), torch.zeros(n, m, dtype=torch.float64)
+    fn = {"none": lambda v: v, "relu": torch.relu, "silu": torch.nn.functional.silu,
+          "gelu": torch.nn.functional.gelu}[act]
+    for j in range(n):
+        for t in range(ids.shape[1]):
+            e = int(ids[j, t])
+            if not 0 <= e < experts:
+                continue
+            u = w1[e] @ x[j]
+            eu = (m + 8) * 2 * U * (w1[e].abs() @ x[j].abs())
+            if b1 is not None:
+                u = u + f64(b1[e])
+                eu = eu + U * (u.abs() + f64(b1[e]).abs())
+            if act != "none":
+                g, eg = fn(u[:hidden]), 1.13 * eu[:hidden]
+                eg = eg + 4 * U * (g.abs() + u[:hidden].abs())
+            else:
+                g, eg = u[:hidden], eu[:hidden]
+            if gated:
+                up, e_up = u[hidden:], eu[hidden:]
+                eg = g.abs() * e_up + (up.abs() + e_up) * eg + U * (g * up).abs()
+                g = g * up
+            eg = eg + 2.0 ** -16 * g.abs()
+            z = w2[e] @ g
+            ez = (hidden + 8) * 4 * U * (w2[e].abs() @ g.abs()) + w2[e].abs() @ eg
+            if b2 is not None:
+                z = z + f64(b2[e])
+                ez = ez + U * (z.abs() + f64(b2[e]).abs())
+            y[j] += wt[j, t] * z
+            b[j] += wt[j, t].abs() * (ez + 2 * (ids.shape[1] + 1) * U * z.abs())
+    return y, b

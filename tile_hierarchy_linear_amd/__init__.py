@@ -1,6 +1,7 @@
 """Python binding of libthl.so: the MI355X tiled GEMM with a fused epilogue,
-the operators around a layer's products (norm, tokens by expert, 4-bit
-weights), and the Shape:Stride layout module.
+the operators around a layer's products (norms, MX quantization, the router,
+tokens by expert, a layer of experts, 4-bit weights), and the Shape:Stride
+layout module.
 
 Argument marshalling only: every step of the GEMM and of the operators runs
 in the library's HIP kernels, and the layout algebra in its C++.  The names
@@ -23,6 +24,8 @@ THL_OP_N, THL_OP_T = 0, 1
 DTYPES = {"f32": 0, "f16": 1, "bf16": 2, "i8": 3, "i32": 4, "e4m3": 5, "e2m1": 6, "e8m0": 7, "none": 8, "e5m2": 9,
           "e2m3": 10, "e3m2": 11, "i4": 12, "u4": 13}
 THL_EPI_NONE, THL_EPI_BIAS, THL_EPI_RELU, THL_EPI_GELU = 0, 1, 2, 4
+THL_ROUTE_SOFTMAX, THL_ROUTE_SIGMOID = 0, 1
+THL_MOE_GATED, THL_MOE_RELU, THL_MOE_GELU, THL_MOE_SILU = 1, 2, 4, 8
 
 
 class ThlError(RuntimeError):
@@ -65,6 +68,17 @@ class thl_norm_grad_types(ctypes.Structure):
 class thl_group_scales(ctypes.Structure):
     _fields_ = [("scales", ctypes.c_void_p), ("ld_scales", ctypes.c_int64), ("zeros", ctypes.c_void_p),
                 ("ld_zeros", ctypes.c_int64), ("group", ctypes.c_int64), ("type", ctypes.c_int)]
+
+
+class thl_route(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("score", ctypes.c_int), ("renormalize", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
+class thl_expert_matrix(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("ld", ctypes.c_int64), ("stride", ctypes.c_int64), ("sf", ctypes.c_void_p),
+                ("ld_sf", ctypes.c_int64), ("stride_sf", ctypes.c_int64), ("bias", ctypes.c_void_p),
+                ("stride_bias", ctypes.c_int64), ("type", ctypes.c_int), ("type_bias", ctypes.c_int)]
 
 
 def _load():
@@ -112,10 +126,23 @@ def _load():
     lib.thl_gemm_w4.argtypes = [i64, i64, i64, vp, i64, ctypes.POINTER(thl_group_scales), vp, i64, vp, i64, vp, i64,
                                 f32, f32, ctypes.POINTER(thl_dtypes), ctypes.POINTER(thl_epilogue), vp, sz, vp]
     lib.thl_gemm_w4_workspace.argtypes = [i64, i64, i64]
-    for name in ("rmsnorm", "rmsnorm_backward", "moe_sort", "moe_gather", "moe_combine", "moe_combine_backward",
+    lib.thl_layernorm.argtypes = [i64, i64, vp, i64, vp, i64, vp, i64, vp, vp, f32, f32, vp, i64, vp, i64,
+                                  ctypes.POINTER(thl_norm_types), vp]
+    lib.thl_layernorm_backward_workspace.argtypes = [i64, i64]
+    lib.thl_layernorm_backward.argtypes = [i64, i64, vp, i64, vp, i64, vp, i64, vp, f32, vp, i64, vp, vp, vp, sz,
+                                           ctypes.POINTER(thl_norm_grad_types), vp]
+    lib.thl_mx_quantize.argtypes = [i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, vp]
+    lib.thl_moe_route.argtypes = [i64, i64, i64, vp, i64, vp, ctypes.POINTER(thl_route), vp, vp, vp]
+    lib.thl_moe_route_backward.argtypes = [i64, i64, i64, vp, i64, ctypes.POINTER(thl_route), vp, vp, vp, i64, vp]
+    lib.thl_moe_layer_workspace.argtypes = [i64, i64, i64, i64]
+    lib.thl_moe_layer.argtypes = [i64, i64, i64, i64, i64, vp, i64, vp, i64, i32, vp, ctypes.POINTER(thl_expert_matrix),
+                                  ctypes.POINTER(thl_expert_matrix), ctypes.c_uint, vp, i64, i32, i32, vp, sz, vp]
+    for name in ("rmsnorm", "rmsnorm_backward", "layernorm", "layernorm_backward", "mx_quantize", "moe_sort",
+                 "moe_gather", "moe_combine", "moe_combine_backward", "moe_route", "moe_route_backward", "moe_layer",
                  "gemm_w4"):
         getattr(lib, "thl_" + name).restype = ctypes.c_int
-    for name in ("rmsnorm_backward_workspace", "moe_sort_workspace", "gemm_w4_workspace"):
+    for name in ("rmsnorm_backward_workspace", "layernorm_backward_workspace", "moe_sort_workspace",
+                 "moe_layer_workspace", "gemm_w4_workspace"):
         getattr(lib, "thl_" + name).restype = sz
     lib.thl_status_string.argtypes = [ctypes.c_int]
     lib.thl_status_string.restype = cp
@@ -335,6 +362,44 @@ def thl_rmsnorm_backward(m, n, S, lds, DY, lddy, DR, lddr, W, eps, DX, lddx, DW,
                                      workspace_bytes, _ref(types), stream)
 
 
+def thl_layernorm(m, n, X, ldx, R, ldr, S, lds, W, B, eps, y_scale, Y, ldy, sfy, ld_sfy, types, stream=None) -> int:
+    return _lib.thl_layernorm(m, n, X, ldx, R, ldr, S, lds, W, B, eps, y_scale, Y, ldy, sfy, ld_sfy, _ref(types),
+                              stream)
+
+
+def thl_layernorm_backward_workspace(m, n) -> int:
+    return _lib.thl_layernorm_backward_workspace(m, n)
+
+
+def thl_layernorm_backward(m, n, S, lds, DY, lddy, DR, lddr, W, eps, DX, lddx, DW, DB, workspace, workspace_bytes,
+                           types, stream=None) -> int:
+    return _lib.thl_layernorm_backward(m, n, S, lds, DY, lddy, DR, lddr, W, eps, DX, lddx, DW, DB, workspace,
+                                       workspace_bytes, _ref(types), stream)
+
+
+def thl_mx_quantize(m, n, X, ldx, Y, ldy, sfy, ld_sfy, YT, ldyt, sfyt, ld_sfyt, type_x, type_y, stream=None) -> int:
+    return _lib.thl_mx_quantize(m, n, X, ldx, Y, ldy, sfy, ld_sfy, YT, ldyt, sfyt, ld_sfyt, _dt(type_x), _dt(type_y),
+                                stream)
+
+
+def thl_moe_route(n, topk, experts, L, ldl, bias, how, ids, weights, stream=None) -> int:
+    return _lib.thl_moe_route(n, topk, experts, L, ldl, bias, _ref(how), ids, weights, stream)
+
+
+def thl_moe_route_backward(n, topk, experts, L, ldl, how, ids, dweights, DL, lddl, stream=None) -> int:
+    return _lib.thl_moe_route_backward(n, topk, experts, L, ldl, _ref(how), ids, dweights, DL, lddl, stream)
+
+
+def thl_moe_layer_workspace(m, hidden, n, topk) -> int:
+    return _lib.thl_moe_layer_workspace(m, hidden, n, topk)
+
+
+def thl_moe_layer(m, hidden, n, topk, experts, X, ldx, ids, ld_ids, ids_bytes, weights, up, down, flags, Y, ldy, type_x,
+                  type_y, workspace, workspace_bytes, stream=None) -> int:
+    return _lib.thl_moe_layer(m, hidden, n, topk, experts, X, ldx, ids, ld_ids, ids_bytes, weights, _ref(up),
+                              _ref(down), flags, Y, ldy, _dt(type_x), _dt(type_y), workspace, workspace_bytes, stream)
+
+
 def thl_moe_sort_workspace(n, topk, experts) -> int:
     return _lib.thl_moe_sort_workspace(n, topk, experts)
 
@@ -416,6 +481,59 @@ def rmsnorm_backward(s, dy, w, dx, dw=None, *, eps=1e-6, dres=None):
     status = _ops.rmsnorm_backward(s, dy, w, dx, dw, eps, dres)
     if status:
         raise ThlError(status, "thl_rmsnorm_backward")
+
+
+def layernorm(x, w, b, y, *, eps=1e-5, residual=None, residual_out=None, scale=1.0, sf=None):
+    """y = the layer norm of x (+ residual) times w plus b (None: ones, zeros), in y's format; otherwise as rmsnorm.
+    Returns y."""
+    status = _ops.layernorm(x, w, b, y, eps, residual, residual_out, scale, sf)
+    if status:
+        raise ThlError(status, "thl_layernorm")
+    return y
+
+
+def layernorm_backward(s, dy, w, dx, dw=None, db=None, *, eps=1e-5, dres=None):
+    """The gradients of layernorm for the s it normalised: dx (of x and residual alike; dres, the gradient that
+    reaches s past the norm, is added) and, if wanted, dw and db (of one type)."""
+    status = _ops.layernorm_backward(s, dy, w, dx, dw, db, eps, dres)
+    if status:
+        raise ThlError(status, "thl_layernorm_backward")
+
+
+def mx_quantize(x, y=None, sf=None, *, y_t=None, sf_t=None):
+    """x as MX blocks of 32 features (y with the E8M0 scales sf) and of 32 tokens of the transposed array (y_t, sf_t),
+    either or both: e4m3 or e5m2 tensors of shapes (tokens, features) and (features, tokens), or uint8 ones of two
+    E2M1 codes a byte."""
+    status = _ops.mx_quantize(x, y, sf, y_t, sf_t)
+    if status:
+        raise ThlError(status, "thl_mx_quantize")
+
+
+def moe_route(logits, ids, weights, *, score="softmax", renormalize=False, scale=1.0, bias=None):
+    """Each token's choice of experts from (tokens, experts) logits, the strongest first: (tokens, choices) int32 ids (-1
+    where masks of -inf or NaN leave none) and fp32 weights, the scores ("softmax" or "sigmoid") of the chosen, divided
+    by their sum with renormalize, times scale.  An fp32 bias a expert is added for the choice alone."""
+    status = _ops.moe_route(logits, ids, weights, score, renormalize, scale, bias)
+    if status:
+        raise ThlError(status, "thl_moe_route")
+
+
+def moe_route_backward(logits, ids, dweights, dlogits, *, score="softmax", renormalize=False, scale=1.0):
+    """moe_route's gradient, the choice held fixed: dlogits (of the logits' type) from the weights' dweights."""
+    status = _ops.moe_route_backward(logits, ids, dweights, dlogits, score, renormalize, scale)
+    if status:
+        raise ThlError(status, "thl_moe_route_backward")
+
+
+def moe_layer(x, ids, weights, w1, w2, y, *, gated=True, act="silu", sf1=None, sf2=None, b1=None, b2=None):
+    """A layer of experts for a few tokens (1,024 choices in all): y = the sum over each token's choices of its weight
+    times expert ids[j, t] of x.  w1 (experts, hidden rows, features; gated: 2 hidden, gates first) and w2 (experts,
+    features, hidden) of x's type, e4m3, or uint8 of two E2M1 codes a byte, with E8M0 scales sf1, sf2 of each 32 values
+    for the last two; biases b1, b2 (experts, rows).  act: "none", "relu", "gelu" or "silu".  Returns y."""
+    status = _ops.moe_layer(x, ids, weights, w1, w2, y, gated, act, sf1, sf2, b1, b2)
+    if status:
+        raise ThlError(status, "thl_moe_layer")
+    return y
 
 
 def moe_sort(ids, experts, rows, offsets, *, order=None):

@@ -1,0 +1,292 @@
+// route.hip -- the router of a layer of experts: each token's choice of
+// experts from its logits with their weights, and the gradient.
+//
+//   p = softmax(l) or sigmoid(l);   the topk experts of the largest p (+ bias)
+//   w_t = scale * p_t,   or scale * p_t / (sum of the chosen p)
+//
+// One wavefront a token, its logits in registers (expert 64 i + lane in
+// register i).  A choice is the largest of 32-bit keys that order like the
+// values: a maximum over the wavefront, then the first register and the first
+// lane that hold it, so that ties go to the lowest expert.  Softmax and
+// sigmoid keep the logits' order, so without a bias the logits themselves are
+// compared, exactly.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <cmath>
+
+#include "../../include/thl.h"
+#include "host_checks.hpp"
+#include "rows.hpp"
+
+namespace thl {
+namespace {
+
+constexpr int64_t kMaxExperts = 1024;
+constexpr int64_t kMaxChoices = 64;
+
+struct RouteArgs {
+  const void* logits;
+  const float* bias;  // NULL: none
+  int32_t* ids;
+  float* weights;
+  const float* dweights;  // gradient only, with dlogits
+  void* dlogits;
+  int64_t ld, ldd, n;
+  int32_t topk, experts, type, score, renormalize;
+  float scale;
+};
+
+__device__ __forceinline__ float wave_sum(float v) {
+  v = sum16(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), s)));
+  return v;
+}
+
+// Unsigned keys that order like the values, equal ones alike (-0 and 0 too);
+// 0 for an expert that cannot be chosen (-infinity or NaN).
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);
+  const uint32_t k = b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+  return v > -INFINITY ? k : 0u;
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return __builtin_bit_cast(float, k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+
+// This token's logits: expert 64 i + lane, -infinity past the last.
+template <int PER>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t row, int lane, float (&l)[PER]) {
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = 64 * i + lane;
+    l[i] = e < a.experts ? load_f(a.logits, a.type, row * a.ld + e) : -INFINITY;
+  }
+}
+
+// The largest logit that is a number above -infinity (the shift of the
+// softmax), and the sum of the exponentials.
+template <int PER>
+__device__ __forceinline__ float softmax_sum(const float (&l)[PER], float top) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) s += l[i] > -INFINITY ? expf(l[i] - top) : 0.0f;
+  return wave_sum(s);
+}
+
+template <int PER>
+__global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int64_t waves = static_cast<int64_t>(gridDim.x) * 4;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); row < a.n; row += waves) {
+    float l[PER];
+    uint32_t key[PER];
+    load_logits<PER>(a, row, lane, l);
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      key[i] = key_of(l[i]);
+      best = max(best, key[i]);
+    }
+    best = wave_max(best);
+    const bool soft = a.score == THL_ROUTE_SOFTMAX;
+    const float top = best ? value_of(best) : 0.0f;
+    // with the chosen ones' sum alone in the quotient, the others' is not needed
+    const float total = soft && (a.bias || !a.renormalize) ? softmax_sum<PER>(l, top) : 1.0f;
+    if (a.bias) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int e = 64 * i + lane;
+        const float p = soft ? expf(l[i] - top) / total : sigmoid(l[i]);
+        key[i] = key[i] && e < a.experts ? key_of(p + a.bias[e]) : 0u;
+      }
+    }
+    int id = -1;  // lane t: choice t
+    for (int t = 0; t < a.topk; ++t) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) most = max(most, key[i]);
+      most = wave_max(most);
+      if (most == 0) break;  // no expert is left
+      int e = -1;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const uint64_t who = __ballot(key[i] == most);
+        if (e < 0 && who) e = 64 * i + __builtin_ctzll(who);
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (64 * i + lane == e) key[i] = 0;
+      if (lane == t) id = e;
+    }
+    float p = 0.0f;
+    if (id >= 0) {
+      const float v = load_f(a.logits, a.type, row * a.ld + id);
+      p = soft ? expf(v - top) / total : sigmoid(v);
+    }
+    const float sum = a.renormalize ? wave_sum(p) : 1.0f;
+    if (lane < a.topk) {
+      a.ids[row * a.topk + lane] = id;
+      a.weights[row * a.topk + lane] = id < 0 || sum == 0.0f ? 0.0f : a.scale * (p / sum);
+    }
+  }
+}
+
+// With w_t = scale * p_t / P (P = 1 where the sum is not divided by) and the
+// gradient g_t of w_t, d p_t = scale * (g_t - sum_c g_c p_c / P) / P, or scale * g_t;
+// then d l = p (d p - sum_e p_e d p_e) for the softmax and d p * p (1 - p) for
+// the sigmoid.
+template <int PER>
+__global__ void __launch_bounds__(256) route_grad_kernel(RouteArgs a) {
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int64_t waves = static_cast<int64_t>(gridDim.x) * 4;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); row < a.n; row += waves) {
+    const bool soft = a.score == THL_ROUTE_SOFTMAX;
+    int id = -1;
+    float g = 0.0f, v = -INFINITY;
+    if (lane < a.topk) {
+      id = a.ids[row * a.topk + lane];
+      if (id < 0 || id >= a.experts) {
+        id = -1;
+      } else {
+        g = a.dweights[row * a.topk + lane];
+        v = load_f(a.logits, a.type, row * a.ld + id);
+      }
+    }
+    float l[PER], top = 0.0f, total = 1.0f;
+    const bool all = soft && !a.renormalize;  // the other experts have a gradient
+    if (all) load_logits<PER>(a, row, lane, l);
+    if (soft) {
+      uint32_t best = key_of(v);
+      if (all) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) best = max(best, key_of(l[i]));
+      }
+      best = wave_max(best);
+      top = best ? value_of(best) : 0.0f;
+      if (all) total = softmax_sum<PER>(l, top);
+    }
+    const float p = id < 0 ? 0.0f : (soft ? expf(v - top) / total : sigmoid(v));
+    const float sum = a.renormalize ? wave_sum(p) : 1.0f;
+    float d = 0.0f, mean = 0.0f;  // d l of this choice, less what all experts share
+    if (a.renormalize) {
+      const float w = sum == 0.0f ? 0.0f : p / sum, along = wave_sum(w * g);
+      if (soft)
+        d = w * (g - along);
+      else
+        d = sum == 0.0f ? 0.0f : w * (g - along) * sigmoid(-v);
+    } else if (soft) {
+      mean = wave_sum(p * g);
+      d = p * g;
+    } else {
+      d = p * g * sigmoid(-v);
+    }
+    d = id < 0 ? 0.0f : a.scale * d;
+    float o[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      o[i] = all && l[i] > -INFINITY ? -a.scale * mean * (expf(l[i] - top) / total) : 0.0f;
+    for (int t = 0; t < a.topk; ++t) {  // in the order of the choices
+      const int e = __shfl(id, t);
+      const float dt = __shfl(d, t);
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (64 * i + lane == e) o[i] += dt;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = 64 * i + lane;
+      if (e >= a.experts) continue;
+      const int64_t at = row * a.ldd + e;
+      if (a.type == THL_F32)
+        static_cast<float*>(a.dlogits)[at] = o[i];
+      else if (a.type == THL_F16)
+        static_cast<_Float16*>(a.dlogits)[at] = static_cast<_Float16>(o[i]);
+      else
+        static_cast<__bf16*>(a.dlogits)[at] = static_cast<__bf16>(o[i]);
+    }
+  }
+}
+
+template <int PER>
+hipError_t launch(RouteArgs& a, hipStream_t st) {
+  const void* f = a.dlogits ? reinterpret_cast<const void*>(&route_grad_kernel<PER>)
+                            : reinterpret_cast<const void*>(&route_kernel<PER>);
+  void* args[] = {&a};
+  const int64_t blocks = (a.n + 3) / 4;
+  return hipLaunchKernel(f, dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536)), dim3(256), args, 0, st);
+}
+hipError_t launch(RouteArgs& a, hipStream_t st) {
+  if (a.experts <= 64) return launch<1>(a, st);
+  if (a.experts <= 128) return launch<2>(a, st);
+  if (a.experts <= 256) return launch<4>(a, st);
+  return a.experts <= 512 ? launch<8>(a, st) : launch<16>(a, st);
+}
+
+bool big(int64_t v) { return v > INT32_MAX; }
+bool off(const void* p, thl_dtype t) { return reinterpret_cast<uintptr_t>(p) % bytes_of(t, 1) != 0; }
+
+thl_status check(int64_t n, int64_t topk, int64_t experts, int64_t ldl, const thl_route* how) {
+  if (!how || n < 0 || topk < 0 || experts < 1) return THL_ERR_INVALID;
+  if (experts > kMaxExperts || topk > kMaxChoices || big(n) || big(ldl)) return THL_ERR_UNSUPPORTED;
+  if (!is_float_io(how->type)) return THL_ERR_UNSUPPORTED;
+  if (how->score != THL_ROUTE_SOFTMAX && how->score != THL_ROUTE_SIGMOID) return THL_ERR_INVALID;
+  if (!std::isfinite(how->scale)) return THL_ERR_INVALID;
+  return ldl < experts ? THL_ERR_INVALID : THL_OK;
+}
+
+}  // namespace
+}  // namespace thl
+
+using namespace thl;
+
+extern "C" {
+
+thl_status thl_moe_route(int64_t n, int64_t topk, int64_t experts, const void* L, int64_t ldl, const float* bias,
+                         const thl_route* how, int32_t* ids, float* weights, struct ihipStream_t* stream) {
+  const thl_status s = check(n, topk, experts, ldl, how);
+  if (s != THL_OK) return s;
+  if (n == 0 || topk == 0) return THL_OK;
+  if (!L || !ids || !weights) return THL_ERR_INVALID;
+  if (off(L, how->type) || off(bias, THL_F32) || off(ids, THL_I32) || off(weights, THL_F32)) return THL_ERR_MISALIGNED;
+  const Range rl = matrix_range(L, how->type, experts, n, ldl), rb = vector_range(bias, experts, 4);
+  const Range ri = vector_range(ids, n * topk, 4), rw = vector_range(weights, n * topk, 4);
+  if (overlaps(ri, rl) || overlaps(ri, rb) || overlaps(rw, rl) || overlaps(rw, rb) || overlaps(ri, rw))
+    return THL_ERR_INVALID;
+  RouteArgs a{};
+  a.logits = L, a.bias = bias, a.ids = ids, a.weights = weights, a.ld = ldl, a.n = n;
+  a.topk = static_cast<int32_t>(topk), a.experts = static_cast<int32_t>(experts), a.type = how->type;
+  a.score = how->score, a.renormalize = how->renormalize != 0, a.scale = how->scale;
+  return launch(a, stream) == hipSuccess ? THL_OK : THL_ERR_HIP;
+}
+
+thl_status thl_moe_route_backward(int64_t n, int64_t topk, int64_t experts, const void* L, int64_t ldl,
+                                  const thl_route* how, const int32_t* ids, const float* dweights, void* DL,
+                                  int64_t lddl, struct ihipStream_t* stream) {
+  const thl_status s = check(n, topk, experts, ldl, how);
+  if (s != THL_OK) return s;
+  if (big(lddl)) return THL_ERR_UNSUPPORTED;
+  if (lddl < experts) return THL_ERR_INVALID;
+  if (n == 0) return THL_OK;
+  if (!L || !DL || (topk > 0 && (!ids || !dweights))) return THL_ERR_INVALID;
+  if (off(L, how->type) || off(DL, how->type) || off(ids, THL_I32) || off(dweights, THL_F32)) return THL_ERR_MISALIGNED;
+  // DL may be L exactly
+  const Range rl = matrix_range(L, how->type, experts, n, ldl), rd = matrix_range(DL, how->type, experts, n, lddl);
+  if ((overlaps(rd, rl) && !(DL == L && lddl == ldl)) || overlaps(rd, vector_range(ids, n * topk, 4)) ||
+      overlaps(rd, vector_range(dweights, n * topk, 4)))
+    return THL_ERR_INVALID;
+  RouteArgs a{};
+  a.logits = L, a.ids = const_cast<int32_t*>(ids), a.dweights = dweights, a.dlogits = DL, a.ld = ldl, a.ldd = lddl;
+  a.n = n, a.topk = static_cast<int32_t>(topk), a.experts = static_cast<int32_t>(experts), a.type = how->type;
+  a.score = how->score, a.renormalize = how->renormalize != 0, a.scale = how->scale;
+  return launch(a, stream) == hipSuccess ? THL_OK : THL_ERR_HIP;
+}
+
+}  // extern "C"

@@ -248,6 +248,7 @@ __device__ __forceinline__ void row_sum(float (&v)[NV], float* slot) {
 typedef uint32_t v2u_a1 __attribute__((ext_vector_type(2), aligned(1)));
 typedef uint32_t u32_a1 __attribute__((aligned(1)));
 typedef uint16_t u16_a1 __attribute__((aligned(1)));
+typedef int v4i_a1 __attribute__((ext_vector_type(4), aligned(1)));
 
 // Codes of eight values (already divided by their scale) in E4M3 or E5M2:
 // round to nearest even, magnitudes past the largest finite value clamped to
@@ -294,4 +295,29 @@ __device__ __forceinline__ void store_codes4(uint8_t* p, uint32_t w, int valid) 
   }
 }
 
+// Eight 16-bit values of which the first `valid` exist, the others zero.
+__device__ __forceinline__ v4i load_x8(const uint16_t* p, int valid) {
+  if (valid >= 8) return *reinterpret_cast<const v4i_a2*>(p);
+  uint32_t u[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < valid) u[e / 2] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
+  return v4i{static_cast<int>(u[0]), static_cast<int>(u[1]), static_cast<int>(u[2]), static_cast<int>(u[3])};
+}
+
+// 16 bytes of codes of which `left` exist; the others read as zero.
+__device__ __forceinline__ void load_codes_at(const uint8_t* p, int64_t left, v4i& o) {
+  o = v4i{0, 0, 0, 0};
+  uint32_t part = 0;
+#pragma unroll
+  for (int q = 0; q < 3; ++q)
+    if (left > 0 && left < 16 && q < (left & 3)) part |= static_cast<uint32_t>(p[(left & 12) + q]) << (8 * q);
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    if (4 * d + 4 <= left)
+      o[d] = static_cast<int>(*reinterpret_cast<const u32_a1*>(p + 4 * d));
+    else if (4 * d < left)
+      o[d] = static_cast<int>(part);
+  }
+}
 }  // namespace thl

@@ -134,6 +134,11 @@ float number(PyObject* o) {
   if (v == -1.0 && PyErr_Occurred()) throw Raised();
   return static_cast<float>(v);
 }
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised();
+  return v != 0;
+}
 const char* text(PyObject* o) {
   const char* s = PyUnicode_AsUTF8(o);
   if (!s) throw Raised();
@@ -215,6 +220,241 @@ thl_status rmsnorm_backward(PyObject* const* a) {
   void* ws = l.take(need);
   return thl_rmsnorm_backward(m, n, ms.p, ms.ld, mg.p, mg.ld, mr.p, mr.ld, pw, eps, mx.p, mx.ld, pd, ws, need, &ty,
                               l.stream);
+}
+
+// x, w, b, y, eps, residual, residual_out, scale, sf
+thl_status layernorm(PyObject* const* a) {
+  const at::Tensor &x = tensor("x", a[0]), &y = tensor("y", a[3]);
+  const int dev = device_of("x", x);
+  const int64_t n = x.size(0), m = x.size(1);
+  const Mat mx = tokens("x", x, dev, n, m);
+  const bool fp4 = y.scalar_type() == at::kByte;
+  Mat my = tokens("y", y, dev, n, fp4 ? (m + 1) / 2 : m), mr, ms, mf;
+  if (fp4) my.ld *= 2;
+  thl_norm_types ty = {static_cast<thl_dtype>(format("x", x)), THL_NONE, THL_NONE,
+                       fp4 ? THL_E2M1X2 : static_cast<thl_dtype>(format("y", y))};
+  void *pw = nullptr, *pb = nullptr;
+  if (given(a[1])) {
+    const at::Tensor& w = tensor("w", a[1]);
+    pw = vec("w", w, dev, m);
+    ty.w = static_cast<thl_dtype>(format("w", w));
+  }
+  if (given(a[2])) {
+    const at::Tensor& b = tensor("b", a[2]);
+    pb = vec("b", b, dev, m);
+    if (pw && format("b", b) != ty.w) throw Refused("b: w's type is expected");
+    ty.w = static_cast<thl_dtype>(format("b", b));
+  }
+  if (given(a[5])) {
+    const at::Tensor& r = tensor("residual", a[5]);
+    mr = tokens("residual", r, dev, n, m);
+    ty.r = static_cast<thl_dtype>(format("residual", r));
+  }
+  if (given(a[6])) {
+    const at::Tensor& s = tensor("residual_out", a[6]);
+    if (!given(a[5]) || format("residual_out", s) != ty.r)
+      throw Refused("residual_out: with a residual, of its type");
+    ms = tokens("residual_out", s, dev, n, m);
+  }
+  if (given(a[8])) mf = byte_rows("sf", tensor("sf", a[8]), dev, n, (m + 31) / 32);
+  const float eps = number(a[4]), scale = number(a[7]);
+  Launch l(dev);
+  return thl_layernorm(m, n, mx.p, mx.ld, mr.p, mr.ld, ms.p, ms.ld, pw, pb, eps, scale, my.p, my.ld,
+                       static_cast<uint8_t*>(mf.p), mf.ld, &ty, l.stream);
+}
+
+// s, dy, w, dx, dw, db, eps, dres
+thl_status layernorm_backward(PyObject* const* a) {
+  const at::Tensor &s = tensor("s", a[0]), &dy = tensor("dy", a[1]), &dx = tensor("dx", a[3]);
+  const int dev = device_of("s", s);
+  const int64_t n = s.size(0), m = s.size(1);
+  const Mat ms = tokens("s", s, dev, n, m), mg = tokens("dy", dy, dev, n, m), mx = tokens("dx", dx, dev, n, m);
+  thl_norm_grad_types ty = {static_cast<thl_dtype>(format("s", s)), THL_NONE, static_cast<thl_dtype>(format("dy", dy)),
+                            THL_NONE};
+  void *pw = nullptr, *pd = nullptr, *pe = nullptr;
+  Mat mr;
+  if (given(a[2])) {
+    const at::Tensor& w = tensor("w", a[2]);
+    pw = vec("w", w, dev, m);
+    ty.w = static_cast<thl_dtype>(format("w", w));
+  }
+  if (format("dx", dx) != ty.g) throw Refused("dx: dy's type is expected");
+  if (given(a[7])) {
+    const at::Tensor& r = tensor("dres", a[7]);
+    if (format("dres", r) != ty.g) throw Refused("dres: dy's type is expected");
+    mr = tokens("dres", r, dev, n, m);
+  }
+  if (given(a[4])) {
+    const at::Tensor& d = tensor("dw", a[4]);
+    pd = vec("dw", d, dev, m);
+    ty.dw = static_cast<thl_dtype>(format("dw", d));
+  }
+  if (given(a[5])) {
+    const at::Tensor& d = tensor("db", a[5]);
+    pe = vec("db", d, dev, m);
+    if (pd && format("db", d) != ty.dw) throw Refused("db: dw's type is expected");
+    ty.dw = static_cast<thl_dtype>(format("db", d));
+  }
+  const float eps = number(a[6]);
+  Launch l(dev);
+  const size_t need = pd || pe ? thl_layernorm_backward_workspace(m, n) : 0;
+  void* ws = l.take(need);
+  return thl_layernorm_backward(m, n, ms.p, ms.ld, mg.p, mg.ld, mr.p, mr.ld, pw, eps, mx.p, mx.ld, pd, pe, ws, need,
+                                &ty, l.stream);
+}
+
+// x, y, sf, y_t, sf_t
+thl_status mx_quantize(PyObject* const* a) {
+  const at::Tensor& x = tensor("x", a[0]);
+  const int dev = device_of("x", x);
+  const int64_t n = x.size(0), m = x.size(1);
+  const Mat mx = tokens("x", x, dev, n, m);
+  Mat out[2], sf[2];
+  int type = THL_NONE;
+  if (given(a[1]) != given(a[2])) throw Refused("y and sf go together");
+  if (given(a[3]) != given(a[4])) throw Refused("y_t and sf_t go together");
+  static const char* const names[2][2] = {{"y", "sf"}, {"y_t", "sf_t"}};
+  for (int i = 0; i < 2; ++i) {
+    if (!given(a[1 + 2 * i])) continue;
+    const at::Tensor& y = tensor(names[i][0], a[1 + 2 * i]);
+    const bool fp4 = y.scalar_type() == at::kByte;
+    const int kind = fp4 ? THL_E2M1X2 : format(names[i][0], y);
+    if (type != THL_NONE && kind != type) throw Refused("y_t: y's type is expected");
+    type = kind;
+    const int64_t rows = i ? m : n, cols = i ? n : m;
+    out[i] = tokens(names[i][0], y, dev, rows, fp4 ? (cols + 1) / 2 : cols);
+    if (fp4) out[i].ld *= 2;
+    sf[i] = byte_rows(names[i][1], tensor(names[i][1], a[2 + 2 * i]), dev, rows, (cols + 31) / 32);
+  }
+  if (type == THL_NONE) throw Refused("y with sf, or y_t with sf_t, is expected");
+  const int type_x = format("x", x);
+  Launch l(dev);
+  return thl_mx_quantize(m, n, mx.p, mx.ld, out[0].p, out[0].ld, static_cast<uint8_t*>(sf[0].p), sf[0].ld, out[1].p,
+                         out[1].ld, static_cast<uint8_t*>(sf[1].p), sf[1].ld, static_cast<thl_dtype>(type_x),
+                         static_cast<thl_dtype>(type), l.stream);
+}
+
+thl_route router(const at::Tensor& logits, PyObject* score, PyObject* renormalize, PyObject* scale) {
+  thl_route how{};
+  how.type = static_cast<thl_dtype>(format("logits", logits));
+  const char* s = text(score);
+  if (strcmp(s, "sigmoid") == 0)
+    how.score = THL_ROUTE_SIGMOID;
+  else if (strcmp(s, "softmax") != 0)
+    throw Refused("score: softmax or sigmoid is expected");
+  how.renormalize = truth(renormalize);
+  how.scale = number(scale);
+  return how;
+}
+
+// logits, ids, weights, score, renormalize, scale, bias
+thl_status moe_route(PyObject* const* a) {
+  const at::Tensor &logits = tensor("logits", a[0]), &ids = tensor("ids", a[1]);
+  const int dev = device_of("logits", logits);
+  const int64_t n = logits.size(0), experts = logits.size(1);
+  if (ids.dim() != 2) throw Refused("ids: (tokens, choices) is expected");
+  const int64_t topk = ids.size(1);
+  const Mat ml = tokens("logits", logits, dev, n, experts);
+  int32_t* pi = static_cast<int32_t*>(table("ids", ids, dev, n, topk, at::kInt));
+  float* pw = static_cast<float*>(table("weights", tensor("weights", a[2]), dev, n, topk, at::kFloat));
+  const thl_route how = router(logits, a[3], a[4], a[5]);
+  const float* pb = nullptr;
+  if (given(a[6])) {
+    const at::Tensor& b = tensor("bias", a[6]);
+    pb = static_cast<const float*>(vec("bias", b, dev, experts));
+    if (b.scalar_type() != at::kFloat) throw Refused("bias: float32 is expected");
+  }
+  Launch l(dev);
+  return thl_moe_route(n, topk, experts, ml.p, ml.ld, pb, &how, pi, pw, l.stream);
+}
+
+// logits, ids, dweights, dlogits, score, renormalize, scale
+thl_status moe_route_backward(PyObject* const* a) {
+  const at::Tensor &logits = tensor("logits", a[0]), &ids = tensor("ids", a[1]), &dl = tensor("dlogits", a[3]);
+  const int dev = device_of("logits", logits);
+  const int64_t n = logits.size(0), experts = logits.size(1);
+  if (ids.dim() != 2) throw Refused("ids: (tokens, choices) is expected");
+  const int64_t topk = ids.size(1);
+  const Mat ml = tokens("logits", logits, dev, n, experts), md = tokens("dlogits", dl, dev, n, experts);
+  if (dl.scalar_type() != logits.scalar_type()) throw Refused("dlogits: the logits' type is expected");
+  const int32_t* pi = static_cast<int32_t*>(table("ids", ids, dev, n, topk, at::kInt));
+  const float* pw = static_cast<float*>(table("dweights", tensor("dweights", a[2]), dev, n, topk, at::kFloat));
+  const thl_route how = router(logits, a[4], a[5], a[6]);
+  Launch l(dev);
+  return thl_moe_route_backward(n, topk, experts, ml.p, ml.ld, &how, pi, pw, md.p, md.ld, l.stream);
+}
+
+// An (experts, rows, k) tensor of weights with its scales and bias.
+thl_expert_matrix experts_of(const char* what, const at::Tensor& w, int dev, int64_t experts, int64_t rows, int64_t k,
+                             const char* what_sf, PyObject* sf, const char* what_b, PyObject* bias) {
+  thl_expert_matrix o{};
+  same_device(what, w, dev);
+  const bool fp4 = w.scalar_type() == at::kByte;
+  const int64_t cols = fp4 ? (k + 1) / 2 : k;
+  if (w.dim() != 3 || w.size(0) != experts || w.size(1) != rows || w.size(2) != cols)
+    throw Refused("%s: a tensor of shape (%lld, %lld, %lld) is expected", what, static_cast<long long>(experts),
+                  static_cast<long long>(rows), static_cast<long long>(cols));
+  if (cols > 1 && w.stride(2) != 1) throw Refused("%s: rows must be contiguous", what);
+  const int64_t packed = fp4 ? 2 : 1;
+  o.w = w.data_ptr();
+  o.ld = packed * (rows > 1 ? w.stride(1) : cols), o.stride = packed * (experts > 1 ? w.stride(0) : 0);
+  o.type = fp4 ? THL_E2M1X2 : static_cast<thl_dtype>(format(what, w));
+  o.type_bias = THL_NONE;
+  if (given(sf)) {
+    const at::Tensor& s = tensor(what_sf, sf);
+    same_device(what_sf, s, dev);
+    const int64_t blocks = (k + 31) / 32;
+    if (s.element_size() != 1 || s.dim() != 3 || s.size(0) != experts || s.size(1) != rows || s.size(2) < blocks ||
+        (blocks > 1 && s.stride(2) != 1))
+      throw Refused("%s: (%lld, %lld) rows of at least %lld bytes are expected", what_sf,
+                    static_cast<long long>(experts), static_cast<long long>(rows), static_cast<long long>(blocks));
+    o.sf = static_cast<const uint8_t*>(s.data_ptr());
+    o.ld_sf = rows > 1 ? s.stride(1) : blocks, o.stride_sf = experts > 1 ? s.stride(0) : 0;
+  }
+  if (given(bias)) {
+    const at::Tensor& b = tensor(what_b, bias);
+    same_device(what_b, b, dev);
+    if (b.dim() != 2 || b.size(0) != experts || b.size(1) != rows || (rows > 1 && b.stride(1) != 1))
+      throw Refused("%s: (%lld, %lld) values are expected", what_b, static_cast<long long>(experts),
+                    static_cast<long long>(rows));
+    o.bias = b.data_ptr(), o.stride_bias = experts > 1 ? b.stride(0) : 0;
+    o.type_bias = static_cast<thl_dtype>(format(what_b, b));
+  }
+  return o;
+}
+
+// x, ids, weights, w1, w2, y, gated, act, sf1, sf2, b1, b2
+thl_status moe_layer(PyObject* const* a) {
+  const at::Tensor &x = tensor("x", a[0]), &ids = tensor("ids", a[1]), &w1 = tensor("w1", a[3]),
+                   &w2 = tensor("w2", a[4]), &y = tensor("y", a[5]);
+  const int dev = device_of("x", x);
+  const int64_t n = x.size(0), m = x.size(1);
+  if (ids.dim() != 2 || (ids.scalar_type() != at::kInt && ids.scalar_type() != at::kLong))
+    throw Refused("ids: (tokens, choices) of int32 or int64 is expected");
+  const int64_t topk = ids.size(1);
+  const Mat mx = tokens("x", x, dev, n, m), my = tokens("y", y, dev, n, m), mi = tokens("ids", ids, dev, n, topk);
+  const float* pw = static_cast<float*>(table("weights", tensor("weights", a[2]), dev, n, topk, at::kFloat));
+  const bool gated = truth(a[6]);
+  if (w1.dim() != 3 || (gated && w1.size(1) % 2 != 0)) throw Refused("w1: (experts, rows, features) is expected");
+  const int64_t experts = w1.size(0), hidden = gated ? w1.size(1) / 2 : w1.size(1);
+  unsigned flags = gated ? THL_MOE_GATED : 0;
+  const char* act = text(a[7]);
+  if (strcmp(act, "relu") == 0)
+    flags |= THL_MOE_RELU;
+  else if (strcmp(act, "gelu") == 0)
+    flags |= THL_MOE_GELU;
+  else if (strcmp(act, "silu") == 0)
+    flags |= THL_MOE_SILU;
+  else if (strcmp(act, "none") != 0)
+    throw Refused("act: none, relu, gelu or silu is expected");
+  const thl_expert_matrix up = experts_of("w1", w1, dev, experts, w1.size(1), m, "sf1", a[8], "b1", a[10]);
+  const thl_expert_matrix down = experts_of("w2", w2, dev, experts, m, hidden, "sf2", a[9], "b2", a[11]);
+  const thl_dtype type_x = static_cast<thl_dtype>(format("x", x)), type_y = static_cast<thl_dtype>(format("y", y));
+  Launch l(dev);
+  const size_t need = thl_moe_layer_workspace(m, hidden, n, topk);
+  void* ws = l.take(need);
+  return thl_moe_layer(m, hidden, n, topk, experts, mx.p, mx.ld, mi.p, mi.ld, static_cast<int>(ids.element_size()), pw,
+                       &up, &down, flags, my.p, my.ld, type_x, type_y, ws, need, l.stream);
 }
 
 // ids, experts, rows, offsets, order
@@ -443,6 +683,12 @@ PyMethodDef method(const char* name) {
 PyMethodDef methods[] = {
     method<rmsnorm, 8, 2, 5, 7>("rmsnorm"),
     method<rmsnorm_backward, 7, 3, 4>("rmsnorm_backward"),
+    method<layernorm, 9, 3, 6, 8>("layernorm"),
+    method<layernorm_backward, 8, 3, 4, 5>("layernorm_backward"),
+    method<mx_quantize, 5, 1, 2, 3, 4>("mx_quantize"),
+    method<moe_route, 7, 1, 2>("moe_route"),
+    method<moe_route_backward, 7, 3>("moe_route_backward"),
+    method<moe_layer, 12, 5>("moe_layer"),
     method<moe_sort, 5, 2, 3, 4>("moe_sort"),
     method<moe_gather, 6, 2, 4>("moe_gather"),
     method<moe_combine, 4, 2>("moe_combine"),

@@ -36,8 +36,6 @@
 namespace thl {
 namespace {
 
-typedef int v4i_a1 __attribute__((ext_vector_type(4), aligned(1)));
-
 struct W4Args {
   const uint8_t* w;
   const void* scales;
@@ -131,16 +129,6 @@ __device__ __forceinline__ v4i in_order(v4i x) {
     o[3] = static_cast<int>(__builtin_amdgcn_perm(x[3], x[1], 0x07060302u));
     return o;
   }
-}
-
-// Eight activations of which the first `valid` exist, the others zero.
-__device__ __forceinline__ v4i load_x8(const uint16_t* p, int valid) {
-  if (valid >= 8) return *reinterpret_cast<const v4i_a2*>(p);
-  uint32_t u[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < valid) u[e / 2] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
-  return v4i{static_cast<int>(u[0]), static_cast<int>(u[1]), static_cast<int>(u[2]), static_cast<int>(u[3])};
 }
 
 // Lane group g (of 16 lanes), register s  <->  lane group s, register g.
@@ -262,21 +250,6 @@ __device__ __forceinline__ float group_offset(const Groups<WT, GPU>& o, int q) {
   return 24.0f;
 }
 
-// 16 bytes of codes of which `left` exist; the others read as zero.
-__device__ __forceinline__ void load_codes_at(const uint8_t* p, int64_t left, v4i& o) {
-  o = v4i{0, 0, 0, 0};
-  uint32_t part = 0;
-#pragma unroll
-  for (int q = 0; q < 3; ++q)
-    if (left > 0 && left < 16 && q < (left & 3)) part |= static_cast<uint32_t>(p[(left & 12) + q]) << (8 * q);
-#pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    if (4 * d + 4 <= left)
-      o[d] = static_cast<int>(*reinterpret_cast<const u32_a1*>(p + 4 * d));
-    else if (4 * d < left)
-      o[d] = static_cast<int>(part);
-  }
-}
 // A lane's codes of the partial unit at K's end, in operand order.
 __device__ __forceinline__ void load_codes_end(const W4Args& a, const uint8_t* row, int u, int g, v4i (&o)[2]) {
 #pragma unroll
