@@ -5,13 +5,13 @@
 //
 // With a few tokens every weight of a chosen expert is used a few times, so
 // the layer is a stream over those weights, bound by HBM.  Nothing is sorted
-// and no size passes through the host: a workgroup takes sixteen features of
-// one expert, finds that expert's choices among the ids itself, and multiplies
-// them, sixteen at a time, on the matrix cores (choices are the rows of the
-// tile, features its columns), its wavefronts splitting K.
-//
-// Three launches: W1 with the activation into the workspace, W2 into the
-// workspace, and the choices of each token added in their order.
+// and no size passes through the host: in the first launch a workgroup takes
+// sixteen features of one expert, finds that expert's choices among the ids
+// itself, and multiplies them on the matrix cores (choices are the rows of the
+// tile, features its columns), its wavefronts splitting K; u goes to the
+// workspace, with each expert's choices.  In the second a workgroup takes
+// sixteen features of all experts, its wavefronts the experts, and adds each
+// token's choices in their order.
 //
 // All products are bf16 by bf16 with fp32 sums, and exact, of one or two
 // planes a side: what has more than eight significant bits (fp16 activations
@@ -20,6 +20,8 @@
 // leaves 2^-17 of the value.  fp16 activations meet fp16 weights as they are.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "../../include/thl.h"
 #include "host_checks.hpp"
@@ -37,6 +39,12 @@ constexpr int kWaves = 4;
 // Values of K in 16 bytes of a row.
 constexpr int piece_of(int wk) { return wk == W_E2M1 ? 32 : (wk == W_E4M3 ? 16 : 8); }
 
+// A slot's choices: their number, where they start in `order`, and their expert.
+struct Slot {
+  uint16_t count, start;
+  int32_t expert;
+};
+
 struct ExpertArgs {
   const uint8_t* w;
   const uint8_t* sf;
@@ -44,16 +52,23 @@ struct ExpertArgs {
   const uint16_t* x;   // X, or u's first plane
   const uint16_t* lo;  // u's second plane
   const void* ids;
-  uint16_t* u_hi;  // outputs: u's planes, or z
+  const float* weights;
+  void* y;
+  // the workspace: u's planes, z of every choice, each slot, and the choices by
+  // expert
+  uint16_t* u_hi;
   uint16_t* u_lo;
   float* z;
+  Slot* slots;
+  int32_t* order;
   int64_t w_row, w_expert;  // bytes
   int64_t ld_sf, sf_expert, bias_expert;
-  int64_t ldx, ld_u, ld_z, ld_ids;
+  int64_t ldx, ldy, ld_u, ld_ids;
   int64_t row_bytes;        // of K weights
   int32_t k, features;      // of an output: hidden features, or the layer's
-  int32_t pairs, topk, experts, ids_bytes, by_choice;
-  int32_t act, bias_type;
+  int32_t pairs, topk, experts, ids_bytes;
+  int32_t slot_count, by_choice;  // a slot is an expert, or where the choices are fewer, a choice
+  int32_t act, bias_type, y_type;
 };
 
 __device__ __forceinline__ int64_t id_of(const ExpertArgs& a, int p) {
@@ -68,24 +83,30 @@ __device__ __forceinline__ v4f mfma_h(v4i a, v4i b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 
-// Eight fp16 numbers as two planes of bf16: the value without its last three
-// bits, and those.  Infinities and NaN have no rest.
+// An fp16 number as two bf16: without its last three bits, and those.
+// Infinities and NaN have no rest.
+__device__ __forceinline__ void split_h1(uint16_t b, uint32_t& hi, uint32_t& lo) {
+  const float f = static_cast<float>(__builtin_bit_cast(_Float16, b));
+  hi = __builtin_bit_cast(uint32_t, f) & 0xffff0000u;
+  lo = __builtin_bit_cast(uint32_t, (b & 0x7c00u) == 0x7c00u ? 0.0f : f - __builtin_bit_cast(float, hi));
+  if ((b & 0x7fffu) > 0x7c00u) hi |= 0x00400000u;  // a NaN stays one
+}
 __device__ __forceinline__ void split_h(v4i x, v4i& hi, v4i& lo) {
 #pragma unroll
   for (int d = 0; d < 4; ++d) {
     uint32_t h[2], l[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const uint16_t b = static_cast<uint16_t>(static_cast<uint32_t>(x[d]) >> (16 * q));
-      const float f = static_cast<float>(__builtin_bit_cast(_Float16, b));
-      h[q] = __builtin_bit_cast(uint32_t, f) & 0xffff0000u;
-      const float rest = (b & 0x7c00u) == 0x7c00u ? 0.0f : f - __builtin_bit_cast(float, h[q]);
-      if ((b & 0x7fffu) > 0x7c00u) h[q] |= 0x00400000u;  // a NaN stays one
-      l[q] = __builtin_bit_cast(uint32_t, rest);
-    }
+    split_h1(static_cast<uint16_t>(x[d]), h[0], l[0]);
+    split_h1(static_cast<uint16_t>(static_cast<uint32_t>(x[d]) >> 16), h[1], l[1]);
     hi[d] = static_cast<int>(__builtin_amdgcn_perm(h[1], h[0], 0x07060302u));
     lo[d] = static_cast<int>(__builtin_amdgcn_perm(l[1], l[0], 0x07060302u));
   }
+}
+__device__ __forceinline__ v4i plane_of(v4i x, bool second) {
+  v4i hi, lo;
+  split_h(x, hi, lo);
+#pragma unroll
+  for (int d = 0; d < 4; ++d) hi[d] = second ? lo[d] : hi[d];
+  return hi;
 }
 
 // u as two planes.
@@ -142,210 +163,394 @@ __device__ __forceinline__ float activated(float v, int act) {
 // order within a lane, so step s of half h multiplies values
 // chunk + PK (4 h + g) + 8 s .. + 7 of choices and features alike.
 //
-// GATED: tiles 0 .. RT/2-1 are gates, the others what they multiply.  UP: the
-// first product (u), else the second (z).
-template <int WK, int XK, bool UP, bool GATED, int RT>
-__global__ void __launch_bounds__(64 * kWaves) experts_kernel(ExpertArgs a) {
-  constexpr int PK = piece_of(WK), KC = 8 * PK, STEPS = PK / 8;
-  constexpr int OUT = GATED ? RT / 2 : RT;  // tiles of outputs
-  constexpr bool MX = WK == W_E4M3 || WK == W_E2M1;
-  constexpr bool HALF = WK == W_H16 && XK == X_H16;  // fp16 by fp16
-  constexpr int XP = XK == X_B16 || HALF ? 1 : 2;
+// A tile's sixteen rows are sixteen choices, or both planes of eight: rows 8 ..
+// 15 then are the second planes of choices 0 .. 7, and their sums are added at
+// the end.  (Planes as products of their own would need twice the operands.)
+template <int WK, int XK>
+struct Kind {
+  static constexpr bool MX = WK == W_E4M3 || WK == W_E2M1;
+  static constexpr bool HALF = WK == W_H16 && XK == X_H16;  // fp16 by fp16
+  static constexpr bool PLANES = XK != X_B16 && !HALF;
+  static constexpr int CAP = PLANES ? 8 : 16;  // choices of a tile
+  static constexpr int PK = piece_of(WK), KC = 8 * PK, STEPS = PK / 8;
+};
+
+// 16 bytes moved `by` (0 or more) towards the first, zeros behind them.
+__device__ __forceinline__ v4i shift_bytes(v4i v, int by) {
+  uint32_t w[4];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) w[d] = static_cast<uint32_t>(v[d]);
+  shift_run<4, 1>(w, by < 16 ? by >> 2 : 8);
+#pragma unroll
+  for (int d = 0; d < 4; ++d)
+    v[d] = static_cast<int>(__builtin_amdgcn_alignbyte(d < 3 ? w[d + 1] : 0u, w[d], by & 3));
+  return v;
+}
+
+// Eight 16-bit values, likewise.
+__device__ __forceinline__ v4i shift_values(v4i v, int by) {
+  uint32_t w[4];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) w[d] = static_cast<uint32_t>(v[d]);
+  shift_run<4, 2>(w, by);
+#pragma unroll
+  for (int d = 0; d < 4; ++d) v[d] = static_cast<int>(w[d]);
+  return v;
+}
+
+// One chunk's weights of RT tiles of features with their scales (of half h in
+// byte g of word h, or bytes 2 h + g / 2), and its activations of MT tiles of
+// choices, as loaded.
+template <int WK, int RT>
+struct Weights {
+  v4i w[2][RT];
+  uint32_t sc[RT][WK == W_E2M1 ? 2 : 1];
+};
+template <int WK, int XK, int MT>
+struct Values {
+  v4i x[2][MT][Kind<WK, XK>::STEPS];
+};
+
+// Chunk c.  `there`: it exists; else every lane loads the matrix's first bytes
+// (a load behind a branch would make the compiler wait for all of them, and a
+// chunk loaded again is traffic).
+template <int WK, int RT>
+__device__ __forceinline__ void load_weights(const ExpertArgs& a, const uint8_t* const (&w)[RT],
+                                             const uint8_t* const (&sf)[RT], int c, bool there, Weights<WK, RT>& o) {
+  const int g = (static_cast<int>(threadIdx.x) & 63) >> 4;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const uint8_t* p = there ? w[r] + 128 * static_cast<int64_t>(c) + 16 * g : a.w;
+    // (not marked to leave L2 first: the two halves of a line come apart)
+    o.w[0][r] = *reinterpret_cast<const v4i_a1*>(p);
+    o.w[1][r] = *reinterpret_cast<const v4i_a1*>(p + 64);
+    if constexpr (WK == W_E2M1) {
+      const v2u_a1 q = *reinterpret_cast<const v2u_a1*>(there ? sf[r] + 8 * static_cast<int64_t>(c) : a.sf);
+      o.sc[r][0] = q[0], o.sc[r][1] = q[1];
+    } else if constexpr (WK == W_E4M3) {
+      o.sc[r][0] = *reinterpret_cast<const u32_a1*>(there ? sf[r] + 4 * static_cast<int64_t>(c) : a.sf);
+    }
+  }
+}
+
+// A wavefront's chunks c0, c0 + step, ... below `whole`, and its first ones on
+// their way: asked for before it is known what they are multiplied with.
+template <int WK, int RT, int D>
+struct Stream {
+  Weights<WK, RT> b[D];
+  int c0, step, whole;
+  bool tail;  // K's partial chunk is this wavefront's
+  __device__ __forceinline__ Stream(const ExpertArgs& a, int first, int by)
+      : c0(first), step(by), whole(a.k / (8 * piece_of(WK))) {
+    tail = whole * 8 * piece_of(WK) < a.k && whole % by == first;
+  }
+  __device__ __forceinline__ int end() const { return c0 + (whole - 1 - c0) / step * step; }
+  __device__ __forceinline__ void start(const ExpertArgs& a, const uint8_t* const (&w)[RT],
+                                        const uint8_t* const (&sf)[RT]) {
+    if (c0 >= whole) return;
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) load_weights<WK, RT>(a, w, sf, c0 + d * step, c0 + d * step < whole, b[d]);
+  }
+};
+
+// The sums over a wavefront's started stream and, if it is its, K's partial
+// chunk, of RT tiles of features (w, sf: this lane's rows) and MT tiles of
+// choices (x: this lane's rows).
+template <int WK, int XK, int RT, int MT, int D>
+__device__ __forceinline__ void products(const ExpertArgs& a, const uint8_t* const (&w)[RT],
+                                         const uint8_t* const (&sf)[RT], const uint16_t* const (&x)[MT],
+                                         Stream<WK, RT, D>& st, v4f (&acc)[RT][MT]) {
+  using T = Kind<WK, XK>;
+  constexpr int PK = T::PK, KC = T::KC, STEPS = T::STEPS;
+  const int lane = static_cast<int>(threadIdx.x) & 63, col = lane & 15, g = lane >> 4;
+  const int c0 = st.c0, step = st.step, whole = st.whole;
+
+  auto operand = [&](v4i v) {
+    if constexpr (XK == X_H16 && !T::HALF) return plane_of(v, col >= 8);
+    return v;
+  };
+  // Half a chunk, `code`: the lane's scales.
+  auto half = [&](const v4i (&wh)[RT], const uint32_t (&code)[RT], const v4i (&xh)[MT][STEPS]) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      v4i xf[MT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) xf[t] = operand(xh[t][s]);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        if constexpr (T::HALF) {
+#pragma unroll
+          for (int t = 0; t < MT; ++t) acc[r][t] = mfma_h(xf[t], wh[r], acc[r][t]);
+        } else if constexpr (WK == W_H16) {
+          v4i hi, lo;
+          split_h(wh[r], hi, lo);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) acc[r][t] = mfma_bf(xf[t], lo, mfma_bf(xf[t], hi, acc[r][t]));
+        } else {
+          v4i q = wh[r];
+          if constexpr (T::MX) q = decode<WK>(q, s, e8m0(code[r]));
+#pragma unroll
+          for (int t = 0; t < MT; ++t) acc[r][t] = mfma_bf(xf[t], q, acc[r][t]);
+        }
+      }
+    }
+  };
+  // The same under scales of which some may take an element out of bf16's normal
+  // numbers: each lane group's blocks by themselves, under a scale next to
+  // their own, and what that lacks applied to the sums.
+  auto half_rare = [&](const v4i (&wh)[RT], const uint32_t (&code)[RT], const v4i (&xh)[MT][STEPS]) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        const float factor = lacking<WK>(static_cast<uint32_t>(__shfl(static_cast<int>(code[r]), 16 * q + col)));
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          v4f alone = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int s = 0; s < STEPS; ++s) {
+            v4i v = decode<WK>(wh[r], s, e8m0(tame<WK>(code[r])));
+            if (g != q) v = v4i{0, 0, 0, 0};
+            alone = mfma_bf(operand(xh[t][s]), v, alone);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[r][t][e] += factor * alone[e];
+        }
+      }
+    }
+  };
+  auto is_rare = [&](const uint32_t (&code)[RT]) {
+    bool any = false;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) any |= code[r] != tame<WK>(code[r]);
+    return __ballot(any) != 0;
+  };
+
+  auto load_x = [&](int c, Values<WK, XK, MT>& o) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+          o.x[h][t][s] = *reinterpret_cast<const v4i_a2*>(x[t] + static_cast<int64_t>(c) * KC + PK * (4 * h + g) + 8 * s);
+  };
+  bool skipped = false;
+  auto use = [&](const Weights<WK, RT>& b, const Values<WK, XK, MT>& v) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t code[RT] = {};
+      if constexpr (T::MX) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          code[r] = (WK == W_E2M1 ? b.sc[r][WK == W_E2M1 ? h : 0] >> (8 * g) : b.sc[r][0] >> (8 * (2 * h + (g >> 1)))) & 255u;
+        if (is_rare(code)) {
+          skipped = true;
+          continue;
+        }
+      }
+      half(b.w[h], code, v.x[h]);
+    }
+  };
+
+  // D - 1 chunks' weights are on their way while one is used.  Its activations,
+  // which L2 holds, are asked for just before: a second set of them would cost
+  // the registers of a wavefront in three and gains nothing.
+  if (c0 < whole) {
+    const int end = st.end();
+    Values<WK, XK, MT> v;
+    for (int c = c0;;) {
+      bool last = false;
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        load_x(c, v);
+        load_weights<WK, RT>(a, w, sf, c + (D - 1) * step, c + (D - 1) * step < whole, st.b[(d + D - 1) % D]);
+        use(st.b[d], v);
+        last = c == end;
+        c += step;
+        if (last) break;
+      }
+      if (last) break;
+    }
+  }
+
+  // The halves that were skipped, and K's partial chunk (whose number is
+  // `whole`).  Loads that would pass a row's end end with it instead and are
+  // shifted into place; rows shorter than a load go element by element.
+  for (int c = skipped ? c0 : whole; c < whole || (c == whole && st.tail); c += step) {
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      const int64_t at = 128 * static_cast<int64_t>(c) + 64 * h + 16 * g, end = a.row_bytes - 16;
+      const int k0 = c * KC + PK * (4 * h + g);
+      v4i wh[RT], xh[MT][STEPS];
+      uint32_t code[RT] = {};
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        if (end >= 0)
+          wh[r] = *reinterpret_cast<const v4i_a1*>(w[r] + (at < end ? at : end));
+        else
+          load_codes_at(w[r] + at, a.row_bytes - at, wh[r]);
+        if constexpr (T::MX) code[r] = sf[r][(k0 < a.k ? k0 : a.k - 1) / 32];
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+          const int k = k0 + 8 * s;
+          if (a.k >= 8)
+            xh[t][s] = *reinterpret_cast<const v4i_a2*>(x[t] + (k < a.k - 8 ? k : a.k - 8));
+          else
+            xh[t][s] = load_x8(x[t] + k, k < a.k ? a.k - k : 0);
+        }
+      if (end >= 0) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) wh[r] = shift_bytes(wh[r], at > end ? static_cast<int>(at - end) : 0);
+      }
+      if (a.k >= 8) {
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+          const int by = k0 + 8 * s - (a.k - 8);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) xh[t][s] = shift_values(xh[t][s], by > 0 ? by : 0);
+        }
+      }
+      bool rare = false;
+      if constexpr (T::MX) {
+        rare = is_rare(code);
+        if (rare) half_rare(wh, code, xh);
+      }
+      if (c == whole && !rare) half(wh, code, xh);
+    }
+  }
+}
+
+// The lane's row of weights of tile r of features f0 .. (`features` in a part;
+// part 1 of a gated matrix is what the gates multiply); features past the last
+// repeat it and are not stored.
+template <int WK>
+__device__ __forceinline__ void row_of(const ExpertArgs& a, int64_t expert, int f, int part, const uint8_t*& w,
+                                       const uint8_t*& sf) {
+  f = f < a.features ? f : a.features - 1;
+  const int64_t row = static_cast<int64_t>(f) + (part ? a.features : 0);
+  w = a.w + expert * a.w_expert + row * a.w_row;
+  sf = WK == W_E4M3 || WK == W_E2M1 ? a.sf + expert * a.sf_expert + row * a.ld_sf : nullptr;
+}
+// The lane's row of activations: of choice `p`, or of its second plane.
+template <int WK, int XK>
+__device__ __forceinline__ const uint16_t* x_of(const ExpertArgs& a, int p, bool second) {
+  if constexpr (XK == X_PAIR) return (second ? a.lo : a.x) + static_cast<int64_t>(p) * a.ldx;
+  return a.x + static_cast<int64_t>(p / a.topk) * a.ldx;
+}
+
+// ---- the first product
+// A workgroup takes OUT tiles of features of one expert; its wavefronts split K.
+template <int WK, int XK, bool GATED, int OUT>
+__global__ void __launch_bounds__(64 * kWaves, 2) experts_up_kernel(ExpertArgs a) {
+  using T = Kind<WK, XK>;
+  constexpr int RT = GATED ? 2 * OUT : OUT, MOST = 2, D = 2;
   __shared__ int list[kMaxPairs];
-  __shared__ int hits[kWaves];
-  __shared__ float part[kWaves][RT][4][64];
+  __shared__ int hits[2][kWaves];
+  __shared__ float part[kWaves][RT][MOST][4][64];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int col = lane & 15, g = lane >> 4;
+  const int col = lane & 15, g = lane >> 4, slot = static_cast<int>(blockIdx.y);
 
-  // This workgroup's expert: the y-th, or that of choice y, if y is the first
-  // choice of it; and its choices in order.
-  int64_t expert = blockIdx.y;
+  // This workgroup's expert: the slot's number, or that of choice `slot`, if it
+  // is the first choice of it; and its choices in order.
+  int64_t expert = slot;
+  bool live = true;
   if (a.by_choice) {
-    expert = id_of(a, static_cast<int>(blockIdx.y));
-    if (expert < 0 || expert >= a.experts) return;
+    expert = id_of(a, slot);
+    live = expert >= 0 && expert < a.experts;
   }
-  int count = 0;
-  for (int base = 0; base < a.pairs; base += 64 * kWaves) {
-    const int p = base + tid;
-    const bool hit = p < a.pairs && id_of(a, p) == expert;
-    const uint64_t who = __ballot(hit);
-    if (lane == 0) hits[wave] = __popcll(who);
-    __syncthreads();
-    int at = count, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      if (w < wave) at += hits[w];
-      all += hits[w];
-    }
-    if (hit) list[at + __popcll(who & ((1ull << lane) - 1))] = p;
-    count += all;
-    __syncthreads();
-  }
-  if (count == 0 || (a.by_choice && list[0] != static_cast<int>(blockIdx.y))) return;
-
-  // Rows of weights: features past the last repeat it, and are not stored.
   const int f0 = static_cast<int>(blockIdx.x) * 16 * OUT;
   const uint8_t* w[RT];
   const uint8_t* sf[RT];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    int f = f0 + 16 * (r % OUT) + col;
-    f = f < a.features ? f : a.features - 1;
-    const int64_t row = static_cast<int64_t>(f) + (GATED && r >= OUT ? a.features : 0);
-    w[r] = a.w + expert * a.w_expert + row * a.w_row;
-    sf[r] = MX ? a.sf + expert * a.sf_expert + row * a.ld_sf : nullptr;
+  for (int r = 0; r < RT; ++r)
+    row_of<WK>(a, live ? expert : 0, f0 + 16 * (r % OUT) + col, GATED && r >= OUT, w[r], sf[r]);
+  Stream<WK, RT, D> st(a, wave, kWaves);
+  // (of a choice that is not its expert's first these loads are for nothing)
+  if (a.by_choice) st.start(a, w, sf);
+  int count = 0, before = 0;  // choices of it, and of experts below it
+  if (live) {
+    for (int base = 0; base < a.pairs; base += 64 * kWaves) {
+      const int p = base + tid;
+      const int64_t id = p < a.pairs ? id_of(a, p) : -1;
+      const bool hit = id == expert;
+      const uint64_t who = __ballot(hit), less = __ballot(id >= 0 && id < expert);
+      if (lane == 0) hits[0][wave] = __popcll(who), hits[1][wave] = __popcll(less);
+      __syncthreads();
+      int at = count, all = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        if (w < wave) at += hits[0][w];
+        all += hits[0][w];
+        before += hits[1][w];
+      }
+      if (hit) list[at + __popcll(who & ((1ull << lane) - 1))] = p;
+      count += all;
+      __syncthreads();
+    }
+    if (a.by_choice && count > 0 && list[0] != slot) count = 0;
   }
-  const int whole = a.k / KC;
+  // (for the second product)
+  if (blockIdx.x == 0) {
+    if (tid == 0)
+      a.slots[slot] = Slot{static_cast<uint16_t>(count), static_cast<uint16_t>(before), static_cast<int32_t>(expert)};
+    for (int i = tid; i < count; i += 64 * kWaves) a.order[before + i] = list[i];
+  }
+  if (count == 0) return;
 
-  for (int first = 0; first < count; first += 16) {
-    const int rows = count - first < 16 ? count - first : 16;
-    const int p = list[first + (col < rows ? col : rows - 1)];
-    const int64_t xrow = XK == X_PAIR ? p : p / a.topk;
-    const uint16_t* x = a.x + xrow * a.ldx;
-    const uint16_t* xl = XK == X_PAIR ? a.lo + xrow * a.ldx : nullptr;
-    v4f acc[RT] = {};
+  if (!a.by_choice) st.start(a, w, sf);
 
-    auto use = [&](const v4i (&wq)[RT][2], const uint32_t (&sc)[RT][2], auto load_x) {
-      bool rare = false;
-      if constexpr (MX) {
+  auto run = [&](int first, auto tiles) {
+    constexpr int MT = decltype(tiles)::value;
+    const uint16_t* x[MT];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) rare |= sc[r][0] != tame<WK>(sc[r][0]) || sc[r][1] != tame<WK>(sc[r][1]);
-        rare = __ballot(rare) != 0;
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        v4f alone[RT][4];  // rare scales: the sums of each lane group's block by themselves
-        if (MX && rare) {
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) alone[r][q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        }
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-          v4i xf[2];
-          load_x(h, s, xf);
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            if constexpr (HALF) {
-              acc[r] = mfma_h(xf[0], wq[r][h], acc[r]);
-            } else if constexpr (WK == W_H16) {
-              v4i hi, lo;
-              split_h(wq[r][h], hi, lo);
-              acc[r] = mfma_bf(xf[0], hi, acc[r]);
-              acc[r] = mfma_bf(xf[0], lo, acc[r]);
-              if constexpr (XP == 2) {
-                acc[r] = mfma_bf(xf[1], hi, acc[r]);
-                acc[r] = mfma_bf(xf[1], lo, acc[r]);
-              }
-            } else if constexpr (WK == W_B16) {
-              acc[r] = mfma_bf(xf[0], wq[r][h], acc[r]);
-              if constexpr (XP == 2) acc[r] = mfma_bf(xf[1], wq[r][h], acc[r]);
-            } else if (!rare) {
-              const v4i v = decode<WK>(wq[r][h], s, e8m0(sc[r][h]));
-              acc[r] = mfma_bf(xf[0], v, acc[r]);
-              if constexpr (XP == 2) acc[r] = mfma_bf(xf[1], v, acc[r]);
-            } else {
-              const v4i v = decode<WK>(wq[r][h], s, e8m0(tame<WK>(sc[r][h])));
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const v4i mine = g == q ? v : v4i{0, 0, 0, 0};
-                alone[r][q] = mfma_bf(xf[0], mine, alone[r][q]);
-                if constexpr (XP == 2) alone[r][q] = mfma_bf(xf[1], mine, alone[r][q]);
-              }
-            }
-          }
-        }
-        if (MX && rare) {
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float factor = lacking<WK>(static_cast<uint32_t>(__shfl(static_cast<int>(sc[r][h]), 16 * q + col)));
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[r][e] += factor * alone[r][q][e];
-            }
-        }
-      }
-    };
-    // The eight values from k on of this lane's choice, as planes.
-    auto planes = [&](v4i v, v4i l, v4i (&xf)[2]) {
-      if constexpr (XK == X_H16 && !HALF) {
-        split_h(v, xf[0], xf[1]);
-      } else {
-        xf[0] = v;
-        xf[1] = l;
-      }
-    };
-
-    for (int c = wave; c < whole; c += kWaves) {
-      v4i wq[RT][2];
-      uint32_t sc[RT][2] = {};
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          wq[r][h] = __builtin_nontemporal_load(
-              reinterpret_cast<const v4i_a1*>(w[r] + 128 * static_cast<int64_t>(c) + 64 * h + 16 * g));
-          if constexpr (MX) sc[r][h] = sf[r][static_cast<int64_t>(c) * (KC / 32) + (4 * h + g) * PK / 32];
-        }
-      use(wq, sc, [&](int h, int s, v4i (&xf)[2]) {
-        const int64_t k = static_cast<int64_t>(c) * KC + PK * (4 * h + g) + 8 * s;
-        v4i v = *reinterpret_cast<const v4i_a2*>(x + k), l = {};
-        if constexpr (XK == X_PAIR) l = *reinterpret_cast<const v4i_a2*>(xl + k);
-        planes(v, l, xf);
-      });
+    for (int t = 0; t < MT; ++t) {
+      const int i = first + T::CAP * t + (T::PLANES ? col & 7 : col);
+      x[t] = x_of<WK, XK>(a, list[i < count ? i : count - 1], T::PLANES && col >= 8);
     }
-    if (whole * KC < a.k && wave == whole % kWaves) {  // K's partial chunk
-      const int c = whole;
-      v4i wq[RT][2];
-      uint32_t sc[RT][2];
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t at = 128 * static_cast<int64_t>(c) + 64 * h + 16 * g;
-          load_codes_at(w[r] + at, a.row_bytes - at, wq[r][h]);
-          sc[r][h] = 127;
-          if constexpr (MX) {
-            const int64_t k = static_cast<int64_t>(c) * KC + (4 * h + g) * PK;
-            if (k < a.k) sc[r][h] = sf[r][k / 32];
-          }
-        }
-      use(wq, sc, [&](int h, int s, v4i (&xf)[2]) {
-        const int64_t k = static_cast<int64_t>(c) * KC + PK * (4 * h + g) + 8 * s, left = a.k - k;
-        const int valid = left < 8 ? static_cast<int>(left < 0 ? 0 : left) : 8;
-        v4i v = load_x8(x + k, valid), l = {};
-        if constexpr (XK == X_PAIR) l = load_x8(xl + k, valid);
-        planes(v, l, xf);
-      });
-    }
-
-    // The wavefronts' sums in their order: register e of lane l is choice
-    // 4 (l / 16) + e and feature l % 16.
-    __syncthreads();
+    v4f acc[RT][MT] = {};
+    products<WK, XK, RT, MT, D>(a, w, sf, x, st, acc);
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) part[wave][r][e][lane] = acc[r][e];
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[wave][r][t][e][lane] = acc[r][t][e];
+  };
+  for (int first = 0; first < count;) {
+    const int left = count - first, tiles = left > T::CAP ? MOST : 1;
+    __syncthreads();  // the sums before these have been read
+    if (tiles == 1)
+      run(first, std::integral_constant<int, 1>{});
+    else
+      run(first, std::integral_constant<int, MOST>{});
     __syncthreads();
-    auto sum = [&](int r) {
-      float v = 0.0f;
-#pragma unroll
-      for (int w2 = 0; w2 < kWaves; ++w2) v += part[w2][r][wave][lane];
-      return v;
-    };
+    // Register e of lane l is choice 4 (l / 16) + e of the tile and feature l % 16.
     static_assert(kWaves == 4, "a wavefront finishes one register");
-    const int row = 4 * g + wave;
+    for (int t = 0; t < tiles; ++t) {
+      const int row = 4 * g + wave, i = T::CAP * t + row;
+      if (row >= T::CAP || i >= left) continue;
+      auto sum = [&](int r) {
+        float v = 0.0f;
 #pragma unroll
-    for (int r = 0; r < OUT; ++r) {
-      const int f = f0 + 16 * r + col;
-      if (row >= rows || f >= a.features) continue;
-      const int64_t at = list[first + row], b = expert * a.bias_expert + f;
-      float v = sum(r);
-      if (a.bias) v += load_f(a.bias, a.bias_type, b);
-      if constexpr (UP) {
+        for (int q = 0; q < kWaves; ++q) {
+          v += part[q][r][t][wave][lane];
+          if constexpr (T::PLANES) v += part[q][r][t][wave][lane + 32];
+        }
+        return v;
+      };
+      const int64_t at = list[first + i];
+#pragma unroll
+      for (int r = 0; r < OUT; ++r) {
+        const int f = f0 + 16 * r + col;
+        if (f >= a.features) continue;
+        const int64_t b = expert * a.bias_expert + f;
+        float v = sum(r);
+        if (a.bias) v += load_f(a.bias, a.bias_type, b);
         v = activated(v, a.act);
         if constexpr (GATED) {
           float m = sum(OUT + r);
@@ -356,57 +561,200 @@ __global__ void __launch_bounds__(64 * kWaves) experts_kernel(ExpertArgs a) {
         split_f(v, hi, lo);
         a.u_hi[at * a.ld_u + f] = hi;
         a.u_lo[at * a.ld_u + f] = lo;
-      } else {
-        a.z[at * a.ld_z + f] = v;
       }
     }
+    first += T::CAP * tiles;
+    if (first < count) st.start(a, w, sf);
   }
 }
 
-struct JoinArgs {
-  const float* z;
-  const float* weights;
-  const void* ids;
-  void* y;
-  int64_t ldy, ld_ids;
-  int32_t m, n, topk, experts, ids_bytes, y_type;
-};
+// ---- the second product
+// The sums of an expert's choices over a wavefront's started stream, handed to
+// `put(place in `order`, choice, tile, feature of it, value)` by the lanes that hold
+// them, planes added.  At most MOST tiles of choices at a time.
+template <int WK, int RT, int D, class Put>
+__device__ __forceinline__ void down_choices(const ExpertArgs& a, const uint8_t* const (&w)[RT],
+                                             const uint8_t* const (&sf)[RT], Stream<WK, RT, D>& st, const int* order,
+                                             int count, Put put) {
+  using T = Kind<WK, X_PAIR>;
+  const int lane = static_cast<int>(threadIdx.x) & 63, col = lane & 15, g = lane >> 4;
+  auto run = [&](int first, auto tiles) {
+    constexpr int MT = decltype(tiles)::value;
+    const uint16_t* x[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const int i = first + T::CAP * t + (col & 7);
+      x[t] = x_of<WK, X_PAIR>(a, order[i < count ? i : count - 1], col >= 8);
+    }
+    v4f acc[RT][MT] = {};
+    products<WK, X_PAIR, RT, MT, D>(a, w, sf, x, st, acc);
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float v = acc[r][t][e] + __shfl_xor(acc[r][t][e], 32);
+          const int i = first + T::CAP * t + 4 * g + e;
+          if (g < 2 && i < count) put(i, order[i], r, col, v);
+        }
+  };
+  for (int first = 0; first < count;) {
+    if (count - first <= T::CAP) {
+      run(first, std::integral_constant<int, 1>{});
+      first += T::CAP;
+    } else {
+      run(first, std::integral_constant<int, 2>{});
+      first += 2 * T::CAP;
+    }
+    if (first < count) st.start(a, w, sf);
+  }
+}
 
-// y_j = the sum over its choices, in their order.
-__global__ void __launch_bounds__(256) experts_join_kernel(JoinArgs a) {
-  const int64_t total = static_cast<int64_t>(a.n) * a.m;
-  for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < total;
-       q += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t j = q / a.m, i = q - j * a.m;
+__device__ __forceinline__ void store_y(const ExpertArgs& a, int64_t j, int64_t f, float v) {
+  const int64_t to = j * a.ldy + f;
+  if (a.y_type == THL_F32)
+    static_cast<float*>(a.y)[to] = v;
+  else if (a.y_type == THL_F16)
+    static_cast<_Float16*>(a.y)[to] = static_cast<_Float16>(v);
+  else
+    static_cast<__bf16*>(a.y)[to] = static_cast<__bf16>(v);
+}
+
+// Few slots: a workgroup takes sixteen features of every slot, its wavefronts
+// the slots (`ks` of them share one slot's K), and adds each token's choices.
+constexpr int kJoinWaves = 8;
+
+template <int WK>
+__global__ void __launch_bounds__(64 * kJoinWaves, 2) experts_down_join_kernel(ExpertArgs a, int ks) {
+  constexpr int D = 2;
+  extern __shared__ int shared[];
+  int* order = shared;
+  int* expert_of = order + a.pairs;                                 // -1: no expert of this layer
+  float* share_of = reinterpret_cast<float*>(expert_of + a.pairs);  // the choices' weights
+  float* z = share_of + a.pairs;                                    // [share of K][choice][feature]
+  const int tid = static_cast<int>(threadIdx.x), col = tid & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int f0 = static_cast<int>(blockIdx.x) * 16, share = wave % ks;
+  float* mine = z + share * a.pairs * 16;
+  bool copied = false;
+  for (int slot = wave / ks; slot < a.slot_count || !copied; slot += kJoinWaves / ks) {
+    const Slot s = slot < a.slot_count ? a.slots[slot] : Slot{0, 0, 0};
+    const uint8_t* w[1];
+    const uint8_t* sf[1];
+    Stream<WK, 1, D> st(a, share, ks);
+    row_of<WK>(a, s.count > 0 ? s.expert : 0, f0 + col, 0, w[0], sf[0]);
+    if (s.count > 0) st.start(a, w, sf);
+    if (!copied) {  // (every wavefront comes here once)
+      for (int i = tid; i < a.pairs; i += 64 * kJoinWaves) {
+        const int64_t e = id_of(a, i);
+        order[i] = a.order[i];
+        expert_of[i] = e >= 0 && e < a.experts ? static_cast<int>(e) : -1;
+        share_of[i] = a.weights[i];
+      }
+      __syncthreads();
+      copied = true;
+    }
+    if (s.count > 0)
+      down_choices<WK, 1, D>(a, w, sf, st, order + s.start, s.count,
+                             [&](int, int p, int, int f, float v) { mine[p * 16 + f] = v; });
+  }
+  __syncthreads();
+  const int n = a.pairs / a.topk;
+  for (int q = tid; q < n * 16; q += 64 * kJoinWaves) {
+    const int j = q >> 4, f = f0 + (q & 15);
+    if (f >= a.features) continue;
     float v = 0.0f;
     for (int t = 0; t < a.topk; ++t) {
-      const int64_t at = j * a.ld_ids + t;
-      const int64_t e = a.ids_bytes == 8 ? static_cast<const int64_t*>(a.ids)[at] : static_cast<const int32_t*>(a.ids)[at];
-      if (e >= 0 && e < a.experts) v += a.weights[j * a.topk + t] * a.z[(j * a.topk + t) * a.m + i];
+      const int p = j * a.topk + t, e = expert_of[p];
+      if (e < 0) continue;
+      float u = 0.0f;
+      for (int i = 0; i < ks; ++i) u += z[(i * a.pairs + p) * 16 + (q & 15)];
+      if (a.bias) u += load_f(a.bias, a.bias_type, e * a.bias_expert + f);
+      v += share_of[p] * u;
     }
-    const int64_t to = j * a.ldy + i;
-    if (a.y_type == THL_F32)
-      static_cast<float*>(a.y)[to] = v;
-    else if (a.y_type == THL_F16)
-      static_cast<_Float16*>(a.y)[to] = static_cast<_Float16>(v);
-    else
-      static_cast<__bf16*>(a.y)[to] = static_cast<__bf16>(v);
+    store_y(a, j, f, v);
   }
 }
 
-template <int WK, int XK, bool UP, bool GATED, int RT>
-hipError_t launch(ExpertArgs& a, hipStream_t st) {
-  constexpr int OUT = 16 * (GATED ? RT / 2 : RT);
-  const int64_t tiles = (static_cast<int64_t>(a.features) + OUT - 1) / OUT;
-  const int slots = a.by_choice ? a.pairs : a.experts;
+// More of them: a workgroup takes RT tiles of features of one slot, its
+// wavefronts splitting K; z goes to the workspace, and a third launch adds
+// each token's choices.
+template <int WK, int RT>
+__global__ void __launch_bounds__(64 * kWaves, 2) experts_down_kernel(ExpertArgs a) {
+  using T = Kind<WK, X_PAIR>;
+  constexpr int D = 2, MOST = 2 * T::CAP;
+  __shared__ float part[kWaves][MOST][16 * RT];
+  const int tid = static_cast<int>(threadIdx.x), col = tid & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Slot slot = a.slots[blockIdx.y];
+  const int count = slot.count;
+  const int* order = a.order + slot.start;
+  if (count == 0) return;
+  const int f0 = static_cast<int>(blockIdx.x) * 16 * RT;
+  const uint8_t* w[RT];
+  const uint8_t* sf[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) row_of<WK>(a, slot.expert, f0 + 16 * r + col, 0, w[r], sf[r]);
+  Stream<WK, RT, D> st(a, wave, kWaves);
+  for (int first = 0; first < count; first += MOST) {
+    st.start(a, w, sf);
+    const int left = count - first < MOST ? count - first : MOST;
+    __syncthreads();  // the sums before these have been read
+    down_choices<WK, RT, D>(a, w, sf, st, order + first, left,
+                            [&](int i, int, int r, int f, float v) { part[wave][i][16 * r + f] = v; });
+    __syncthreads();
+    for (int q = tid; q < left * 16 * RT; q += 64 * kWaves) {
+      const int i = q / (16 * RT), f = q % (16 * RT);
+      if (f0 + f >= a.features) continue;
+      float v = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) v += part[k][i][f];
+      a.z[static_cast<int64_t>(order[first + i]) * a.features + f0 + f] = v;
+    }
+  }
+}
+
+// y_j = the sum over its choices, in their order: four choices' loads at a time
+// (of a choice that does not count they are of what is there, and not used).
+__global__ void __launch_bounds__(256) experts_join_kernel(ExpertArgs a) {
+  const int64_t m = a.features, total = static_cast<int64_t>(a.pairs / a.topk) * m;
+  for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < total;
+       q += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t j = q / m, f = q - j * m, base = j * a.topk;
+    float v = 0.0f;
+    for (int t0 = 0; t0 < a.topk; t0 += 4) {
+      int64_t e[4];
+      float weight[4], z[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t p = base + (t0 + i < a.topk ? t0 + i : t0);
+        e[i] = id_of(a, static_cast<int>(p));
+        weight[i] = a.weights[p];
+        z[i] = a.z[p * m + f];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (t0 + i >= a.topk || e[i] < 0 || e[i] >= a.experts) continue;
+        if (a.bias) z[i] += load_f(a.bias, a.bias_type, e[i] * a.bias_expert + f);
+        v += weight[i] * z[i];
+      }
+    }
+    store_y(a, j, f, v);
+  }
+}
+
+template <int WK, int XK, bool GATED>
+hipError_t launch_up(ExpertArgs& a, hipStream_t st) {
   void* args[] = {&a};
-  return hipLaunchKernel(reinterpret_cast<const void*>(&experts_kernel<WK, XK, UP, GATED, RT>),
-                         dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(slots)), dim3(64 * kWaves), args, 0,
-                         st);
+  const int64_t tiles = (static_cast<int64_t>(a.features) + 15) / 16;
+  return hipLaunchKernel(reinterpret_cast<const void*>(&experts_up_kernel<WK, XK, GATED, 1>),
+                         dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.slot_count)), dim3(64 * kWaves),
+                         args, 0, st);
 }
 template <int WK, int XK>
 hipError_t launch_up(ExpertArgs& a, bool gated, hipStream_t st) {
-  return gated ? launch<WK, XK, true, true, 2>(a, st) : launch<WK, XK, true, false, 2>(a, st);
+  return gated ? launch_up<WK, XK, true>(a, st) : launch_up<WK, XK, false>(a, st);
 }
 hipError_t launch_up(ExpertArgs& a, thl_dtype w, bool x_bf, bool gated, hipStream_t st) {
   switch (w) {
@@ -420,16 +768,37 @@ hipError_t launch_up(ExpertArgs& a, thl_dtype w, bool x_bf, bool gated, hipStrea
       return x_bf ? launch_up<W_E2M1, X_B16>(a, gated, st) : launch_up<W_E2M1, X_H16>(a, gated, st);
   }
 }
+
+template <int WK>
+hipError_t launch_down(ExpertArgs& a, hipStream_t st) {
+  const int64_t tiles = (static_cast<int64_t>(a.features) + 15) / 16;
+  if (a.slot_count <= 16 && a.pairs <= 512) {
+    int ks = 1;
+    while (2 * ks * a.slot_count <= kJoinWaves && 2 * ks * a.pairs <= 512) ks *= 2;
+    void* args[] = {&a, &ks};
+    return hipLaunchKernel(reinterpret_cast<const void*>(&experts_down_join_kernel<WK>),
+                           dim3(static_cast<unsigned>(tiles)), dim3(64 * kJoinWaves), args,
+                           static_cast<unsigned>(4 * a.pairs * (3 + 16 * ks)), st);
+  }
+  void* args[] = {&a};
+  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(&experts_down_kernel<WK, 2>),
+                                       dim3(static_cast<unsigned>((tiles + 1) / 2), static_cast<unsigned>(a.slot_count)),
+                                       dim3(64 * kWaves), args, 0, st);
+  if (e != hipSuccess) return e;
+  const int64_t blocks = (static_cast<int64_t>(a.pairs / a.topk) * a.features + 255) / 256;
+  return hipLaunchKernel(reinterpret_cast<const void*>(&experts_join_kernel),
+                         dim3(static_cast<unsigned>(blocks < 8192 ? blocks : 8192)), dim3(256), args, 0, st);
+}
 hipError_t launch_down(ExpertArgs& a, thl_dtype w, hipStream_t st) {
   switch (w) {
     case THL_BF16:
-      return launch<W_B16, X_PAIR, false, false, 2>(a, st);
+      return launch_down<W_B16>(a, st);
     case THL_F16:
-      return launch<W_H16, X_PAIR, false, false, 2>(a, st);
+      return launch_down<W_H16>(a, st);
     case THL_E4M3:
-      return launch<W_E4M3, X_PAIR, false, false, 2>(a, st);
+      return launch_down<W_E4M3>(a, st);
     default:
-      return launch<W_E2M1, X_PAIR, false, false, 2>(a, st);
+      return launch_down<W_E2M1>(a, st);
   }
 }
 
@@ -480,7 +849,7 @@ extern "C" {
 size_t thl_moe_layer_workspace(int64_t m, int64_t hidden, int64_t n, int64_t topk) {
   if (m <= 0 || m > kMaxFeatures || hidden <= 0 || hidden > kMaxFeatures || n <= 0 || topk <= 0) return 0;
   if (n > kMaxPairs || topk > kMaxPairs || n * topk > kMaxPairs) return 0;
-  return static_cast<size_t>(n * topk) * 4 * static_cast<size_t>(pitch(hidden) + m);
+  return static_cast<size_t>(n * topk) * 4 * static_cast<size_t>(pitch(hidden) + m + 3);
 }
 
 thl_status thl_moe_layer(int64_t m, int64_t hidden, int64_t n, int64_t topk, int64_t experts, const void* X,
@@ -531,11 +900,12 @@ thl_status thl_moe_layer(int64_t m, int64_t hidden, int64_t n, int64_t topk, int
   ExpertArgs a{};
   a.ids = ids, a.ld_ids = ld_ids, a.ids_bytes = ids_bytes;
   a.pairs = static_cast<int32_t>(pairs), a.topk = static_cast<int32_t>(topk), a.experts = static_cast<int32_t>(experts);
-  // a workgroup for each choice where they are fewer than the experts (grid rows)
   a.by_choice = pairs < experts;
-  a.u_hi = static_cast<uint16_t*>(workspace), a.u_lo = a.u_hi + pairs * ld_u;
+  a.slot_count = a.by_choice ? a.pairs : a.experts;
+  a.weights = weights, a.y = Y, a.ldy = ldy, a.y_type = type_y;
+  a.u_hi = static_cast<uint16_t*>(workspace), a.u_lo = a.u_hi + pairs * ld_u, a.ld_u = ld_u;
   a.z = reinterpret_cast<float*>(a.u_lo + pairs * ld_u);
-  a.ld_u = ld_u, a.ld_z = m;
+  a.slots = reinterpret_cast<Slot*>(a.z + pairs * m), a.order = reinterpret_cast<int32_t*>(a.slots + pairs);
 
   matrix(a, *up, m);
   a.x = static_cast<const uint16_t*>(X), a.ldx = ldx, a.features = static_cast<int32_t>(hidden);
@@ -545,16 +915,6 @@ thl_status thl_moe_layer(int64_t m, int64_t hidden, int64_t n, int64_t topk, int
     matrix(a, *down, hidden);
     a.x = a.u_hi, a.lo = a.u_lo, a.ldx = ld_u, a.features = static_cast<int32_t>(m);
     e = launch_down(a, down->type, stream);
-  }
-  if (e == hipSuccess) {
-    JoinArgs j{};
-    j.z = a.z, j.weights = weights, j.ids = ids, j.y = Y, j.ldy = ldy, j.ld_ids = ld_ids;
-    j.m = static_cast<int32_t>(m), j.n = static_cast<int32_t>(n), j.topk = a.topk, j.experts = a.experts;
-    j.ids_bytes = ids_bytes, j.y_type = type_y;
-    void* args[] = {&j};
-    const int64_t blocks = (n * m + 255) / 256;
-    e = hipLaunchKernel(reinterpret_cast<const void*>(&experts_join_kernel),
-                        dim3(static_cast<unsigned>(blocks < 8192 ? blocks : 8192)), dim3(256), args, 0, stream);
   }
   return e == hipSuccess ? THL_OK : THL_ERR_HIP;
 }
