@@ -375,15 +375,35 @@ __global__ void __launch_bounds__(WPR * tokens_at_once(WPR) * 64) norm_grad_kern
     const void* dr = a.dr ? a.dr : a.dy;
     const int64_t lddr = a.dr ? a.lddr : a.lddy;
     const int64_t step = static_cast<int64_t>(gridDim.x) * TOKENS;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * TOKENS + which; row < a.n; row += step, parity ^= 1) {
-      Raw8<SB> sr[NC];
-      Raw8<GB> gr[NC], rr[NC];
+    Raw8<SB> sr[NC];
+    Raw8<GB> gr[NC], rr[NC];
+    auto load_row = [&](int64_t row, Raw8<SB> (&s)[NC], Raw8<GB> (&g)[NC], Raw8<GB> (&r)[NC]) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int e = 8 * (t + T * c);
-        sr[c] = load_run<SB, RUNS>(a.s, row * a.lds, e, m);
-        gr[c] = load_run<GB, RUNS>(a.dy, row * a.lddy, e, m);
-        rr[c] = load_run<GB, RUNS>(dr, row * lddr, e, m);
+        s[c] = load_run<SB, RUNS>(a.s, row * a.lds, e, m);
+        g[c] = load_run<GB, RUNS>(a.dy, row * a.lddy, e, m);
+        r[c] = load_run<GB, RUNS>(dr, row * lddr, e, m);
+      }
+    };
+    // Centred, with a second sum across the workgroup, a token waits long enough
+    // to ask for the next one first (the last one asks for itself again): 8,192 x
+    // 4,096 bf16 with dr 58 us for 66.  Two runs a lane on sixteen wavefronts
+    // have no registers for it.
+    constexpr bool AHEAD = CENTRED && WPR <= 8;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * TOKENS + which;
+    Raw8<SB> sn[AHEAD ? NC : 1];
+    Raw8<GB> gn[AHEAD ? NC : 1], rn[AHEAD ? NC : 1];
+    if constexpr (AHEAD) {
+      if (row0 < a.n) load_row(row0, sn, gn, rn);
+    }
+    for (int64_t row = row0; row < a.n; row += step, parity ^= 1) {
+      if constexpr (AHEAD) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) sr[c] = sn[c], gr[c] = gn[c], rr[c] = rn[c];
+        load_row(row + step < a.n ? row + step : row, sn, gn, rn);
+      } else {
+        load_row(row, sr, gr, rr);
       }
       float s[NC][8], g[NC][8], sum[NS] = {};
       if constexpr (CENTRED) {
