@@ -202,6 +202,65 @@ def test_scales_beyond_normal_bf16(w, lo, hi):
 
 
 @pytest.mark.parametrize("w", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+@pytest.mark.parametrize("lo,hi", [(60, 66), (98, 112), (104, 127), (120, 140), (190, 196)])
+def test_every_code_under_every_scale(w, x, lo, hi):
+    """One value in each token, and a second matrix that passes u on: the elements themselves, bit for bit."""
+    g = torch.Generator().manual_seed(hi)
+    for m, hidden in ((256, 64), (150, 96)):
+        sf = torch.randint(lo, hi, (1, hidden, -(-m // 32)), generator=g).to(torch.uint8)
+        if w == "e2m1":
+            codes = torch.randint(0, 256, (hidden, m // 2), generator=g).to(torch.uint8)
+            v1, w1 = ref.e2m1_values(codes, m), codes[None]
+            w2 = torch.zeros(1, m, hidden, dtype=torch.uint8)
+            w2[0, torch.arange(hidden), torch.arange(hidden)] = 2  # 1
+            w2 = w2[:, :, 0::2] | (w2[:, :, 1::2] << 4)
+        else:
+            codes = torch.randint(0, 256, (hidden, m), generator=g).to(torch.uint8)
+            codes[(codes & 0x7F) == 0x7F] = 1  # no NaN; the smallest
+            w1 = codes[None].view(F["e4m3"])
+            v1 = ref.f64(w1)[0]
+            w2 = torch.zeros(1, m, hidden)
+            w2[0, torch.arange(hidden), torch.arange(hidden)] = 1.0
+            w2 = w2.to(F["e4m3"])
+        v1 = v1 * torch.pow(2.0, sf[0].double() - 127).repeat_interleave(32, dim=1)[:, :m]
+        xt = torch.diag(torch.tensor([1.0, -2.0, 0.5]).repeat(m)[:m]).to(F[x])
+        y = torch.full((m, m), float("nan"), device=DEV)
+        thl.moe_layer(xt.to(DEV), torch.zeros(m, 1, dtype=torch.int32, device=DEV), torch.ones(m, 1, device=DEV),
+                      w1.to(DEV), w2.to(DEV), y, gated=False, act="none", sf1=sf.to(DEV),
+                      sf2=torch.full((1, m, -(-hidden // 32)), 127, dtype=torch.uint8, device=DEV))
+        torch.cuda.synchronize()
+        want = torch.zeros(m, m, dtype=torch.float64)
+        want[:, :hidden] = xt.double() @ v1.T
+        assert torch.equal(y.cpu().double(), want)
+
+
+@pytest.mark.parametrize("w", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+@pytest.mark.parametrize("rare", [3, 250])
+@pytest.mark.parametrize("m", [100, 256, 300])
+def test_infinities_next_to_extreme_scales(w, x, rare, m):
+    # every weight 1 or 2^(rare - 127), one activation infinite, the others 0: every sum is that infinity
+    hidden = 32
+    one = {"e2m1": 0x22, "e4m3": 0x38}[w]
+    w1, w2 = (torch.full((1, r, k // 2 if w == "e2m1" else k), one, dtype=torch.uint8, device=DEV)
+              for r, k in ((hidden, m), (m, hidden)))
+    if w == "e4m3":
+        w1, w2 = w1.view(F["e4m3"]), w2.view(F["e4m3"])
+    xt = torch.zeros(3, m, dtype=F[x], device=DEV)
+    xt[0, 5], xt[1, m - 1] = float("inf"), float("-inf")
+    for block in range(-(-m // 32)):
+        sf1 = torch.full((1, hidden, -(-m // 32)), 127, dtype=torch.uint8, device=DEV)
+        sf1[:, :, block] = rare
+        y = torch.empty(3, m, device=DEV)
+        thl.moe_layer(xt, torch.zeros(3, 1, dtype=torch.int32, device=DEV), torch.ones(3, 1, device=DEV), w1, w2, y,
+                      gated=False, act="none", sf1=sf1,
+                      sf2=torch.full((1, m, 1), 127, dtype=torch.uint8, device=DEV))
+        torch.cuda.synchronize()
+        assert bool((y[0] == float("inf")).all()) and bool((y[1] == float("-inf")).all()) and bool((y[2] == 0).all())
+
+
+@pytest.mark.parametrize("w", ["e2m1", "e4m3"])
 def test_a_nan_scale(w):
     xt, ids, wt, w1, w2, yt, call = _layer(3, 300, 64, 2, 1, w=w, ids=torch.tensor([[0], [1], [0]]))
     sf1 = call["sf1"].clone()

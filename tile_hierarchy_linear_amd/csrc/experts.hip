@@ -9,15 +9,21 @@
 // sixteen features of one expert, finds that expert's choices among the ids
 // itself, and multiplies them on the matrix cores (choices are the rows of the
 // tile, features its columns), its wavefronts splitting K; u goes to the
-// workspace, with each expert's choices.  In the second a workgroup takes
-// sixteen features of all experts, its wavefronts the experts, and adds each
-// token's choices in their order.
+// workspace, with each expert's choices.  The second launch does the same with
+// the second matrix, and a third adds each token's choices in their order; for
+// few bytes of weights one launch does both.
 //
-// All products are bf16 by bf16 with fp32 sums, and exact, of one or two
-// planes a side: what has more than eight significant bits (fp16 activations
-// and weights; u, which is computed in fp32) is a sum of two bf16 numbers, its
-// value rounded to eight bits and the rest.  For fp16 that is exact; for u it
-// leaves 2^-17 of the value.  fp16 activations meet fp16 weights as they are.
+// Products are exact and their sums fp32.  The first multiplies activations of
+// bf16 or fp16 with weights of their type, or MX weights decoded to it.  u is
+// computed in fp32 and taken as a sum of two bf16 numbers, its value rounded to
+// eight bits and the rest, which leaves 2^-17 of the value; the second product
+// adds those of both, and fp16 weights are, exactly, two bf16 numbers as well.
+// (fp16 for u would do for its bits but not for its range.)
+//
+// Measured, silu, gated, bf16 activations: one token of 4096 features, 8 of 128
+// experts of 1024 E2M1, 20.9 us (13 and 9; its 53 MB at what HBM copies are 9,
+// and a wavefront's 8 KB of weights come after its ids, so two latencies are
+// most of each launch).  48 tokens, 64 experts of bf16, 1.6 GB, 285 us: 5.6 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -35,6 +41,15 @@ enum : int { X_B16 = 0, X_H16 = 1, X_PAIR = 2 };  // PAIR: u as two planes
 
 constexpr int64_t kMaxPairs = 1024;  // choices of all tokens
 constexpr int kWaves = 4;
+
+// Tiles of choices that share a pass over an expert's weights.  A second one
+// needs its activations, four times as many registers of them for E2M1 as for
+// 16-bit weights, and costs wavefronts; without it an expert of more choices than
+// a tile's is read again, from L2.  Both, of 64 experts of 2048 x 768, 4 and 16
+// choices each, first product: E2M1 30.7 and 72.6 us with one tile, 34.6 and
+// 69.6 with two; E4M3 50.2 and 117.6, 53.1 and 97.0.  bf16 with 128 experts,
+// 3 choices each: 112.9 with one, 103.9 with two.
+constexpr int most_tiles(int wk) { return wk == W_E2M1 ? 1 : 2; }
 
 // Values of K in 16 bytes of a row.
 constexpr int piece_of(int wk) { return wk == W_E2M1 ? 32 : (wk == W_E4M3 ? 16 : 8); }
@@ -101,14 +116,6 @@ __device__ __forceinline__ void split_h(v4i x, v4i& hi, v4i& lo) {
     lo[d] = static_cast<int>(__builtin_amdgcn_perm(l[1], l[0], 0x07060302u));
   }
 }
-__device__ __forceinline__ v4i plane_of(v4i x, bool second) {
-  v4i hi, lo;
-  split_h(x, hi, lo);
-#pragma unroll
-  for (int d = 0; d < 4; ++d) hi[d] = second ? lo[d] : hi[d];
-  return hi;
-}
-
 // u as two planes.
 __device__ __forceinline__ void split_f(float v, uint16_t& hi, uint16_t& lo) {
   const __bf16 h = static_cast<__bf16>(v);
@@ -117,39 +124,57 @@ __device__ __forceinline__ void split_f(float v, uint16_t& hi, uint16_t& lo) {
   lo = __builtin_fabsf(f) < INFINITY ? __builtin_bit_cast(uint16_t, static_cast<__bf16>(v - f)) : 0;
 }
 
-// Codes 8 s .. 8 s + 7 of a piece as bf16, times `scale`, a power of two.
-template <int WK>
+// Codes 8 s .. 8 s + 7 of a piece, times `scale`, a power of two: as fp16 if H,
+// else as bf16.
+template <int WK, bool H>
 __device__ __forceinline__ v4i decode(v4i w, int s, float scale) {
   v4i o;
+#define THL_TWO(i, codes, which)                                                                            \
+  if constexpr (WK == W_E2M1 && H)                                                                          \
+    o[i] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, which));          \
+  else if constexpr (WK == W_E2M1)                                                                          \
+    o[i] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, which));         \
+  else if constexpr (H)                                                                                     \
+    o[i] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, scale, (which) != 0));   \
+  else                                                                                                      \
+    o[i] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, (which) != 0))
   if constexpr (WK == W_E2M1) {
     const uint32_t v = static_cast<uint32_t>(w[s]);
-    o[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 0));
-    o[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 1));
-    o[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 2));
-    o[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, scale, 3));
+    THL_TWO(0, v, 0);
+    THL_TWO(1, v, 1);
+    THL_TWO(2, v, 2);
+    THL_TWO(3, v, 3);
   } else {
     const uint32_t a = static_cast<uint32_t>(w[2 * s]), b = static_cast<uint32_t>(w[2 * s + 1]);
-    o[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, false));
-    o[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, true));
-    o[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, false));
-    o[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, true));
+    THL_TWO(0, a, 0);
+    THL_TWO(1, a, 1);
+    THL_TWO(2, b, 0);
+    THL_TWO(3, b, 1);
   }
+#undef THL_TWO
   return o;
 }
 
-// E8M0 code 1 .. 254 in fp32: 2^(b - 127).
-__device__ __forceinline__ float e8m0(uint32_t b) { return __builtin_bit_cast(float, b << 23); }
-// The scale next to this one under which every element is a normal bf16
-// number, and what it lacks: a factor of the sums.
-template <int WK>
-__device__ __forceinline__ uint32_t tame(uint32_t b) {
-  constexpr uint32_t lo = WK == W_E2M1 ? 2 : 10, hi = WK == W_E2M1 ? 252 : 246;
-  return b < lo ? lo : (b > hi ? hi : b);
-}
-template <int WK>
-__device__ __forceinline__ float lacking(uint32_t b) {
-  return b == 255 ? __builtin_nanf("") : __builtin_bit_cast(float, (127 + b - tame<WK>(b)) << 23);
-}
+// fp32 numbers by their exponent: 2^(e - 127), e from 1 to 254.
+__device__ __forceinline__ float exp2_of(uint32_t e) { return __builtin_bit_cast(float, e << 23); }
+
+// MX blocks are decoded with 2^SHIFT times their scale, and the sums divided by
+// it.  An E8M0 code b = LO .. HI so makes every element a number of the type:
+// a normal bf16 number, or an fp16 number (of E4M3, down to its subnormal ones).
+// With SHIFT the 23 to 27 powers of two that fp16 has room for lie where
+// weights' scales do: maxima from 2^-15 to 2^8 or 2^-17 to 2^10.
+template <int WK, bool H>
+struct Scales {
+  static constexpr int SHIFT = !H ? 0 : (WK == W_E2M1 ? 6 : 8);
+  static constexpr uint32_t LO = !H ? (WK == W_E2M1 ? 2 : 10) : (WK == W_E2M1 ? 127 - 13 - SHIFT : 127 - 15 - SHIFT);
+  static constexpr uint32_t HI = !H ? (WK == W_E2M1 ? 252 : 246) : (WK == W_E2M1 ? 127 + 13 - SHIFT : 127 + 7 - SHIFT);
+  // The code next to b in that range, and what a sum decoded under it lacks.
+  static __device__ __forceinline__ uint32_t tame(uint32_t b) { return b < LO ? LO : (b > HI ? HI : b); }
+  static __device__ __forceinline__ float lacking(uint32_t b) {
+    return b == 255 ? __builtin_nanf("") : exp2_of(127 + b - tame(b) - SHIFT);
+  }
+  static __device__ __forceinline__ float decoding(uint32_t b) { return exp2_of(b + SHIFT); }
+};
 
 __device__ __forceinline__ float activated(float v, int act) {
   if (act & THL_MOE_RELU) return v > 0.0f ? v : 0.0f;
@@ -163,14 +188,14 @@ __device__ __forceinline__ float activated(float v, int act) {
 // order within a lane, so step s of half h multiplies values
 // chunk + PK (4 h + g) + 8 s .. + 7 of choices and features alike.
 //
-// A tile's sixteen rows are sixteen choices, or both planes of eight: rows 8 ..
-// 15 then are the second planes of choices 0 .. 7, and their sums are added at
-// the end.  (Planes as products of their own would need twice the operands.)
+// A tile's sixteen rows are sixteen choices, or of u both planes of eight: rows
+// 8 .. 15 then are the second planes of choices 0 .. 7, and their sums are added
+// at the end.  (Planes as products of their own would need twice the operands.)
 template <int WK, int XK>
 struct Kind {
   static constexpr bool MX = WK == W_E4M3 || WK == W_E2M1;
-  static constexpr bool HALF = WK == W_H16 && XK == X_H16;  // fp16 by fp16
-  static constexpr bool PLANES = XK != X_B16 && !HALF;
+  static constexpr bool HALF = XK == X_H16;  // fp16 by fp16; else bf16 by bf16
+  static constexpr bool PLANES = XK == X_PAIR;
   static constexpr int CAP = PLANES ? 8 : 16;  // choices of a tile
   static constexpr int PK = piece_of(WK), KC = 8 * PK, STEPS = PK / 8;
 };
@@ -262,56 +287,50 @@ __device__ __forceinline__ void products(const ExpertArgs& a, const uint8_t* con
                                          Stream<WK, RT, D>& st, v4f (&acc)[RT][MT]) {
   using T = Kind<WK, XK>;
   constexpr int PK = T::PK, KC = T::KC, STEPS = T::STEPS;
+  using S = Scales<WK, T::HALF>;
   const int lane = static_cast<int>(threadIdx.x) & 63, col = lane & 15, g = lane >> 4;
   const int c0 = st.c0, step = st.step, whole = st.whole;
 
-  auto operand = [&](v4i v) {
-    if constexpr (XK == X_H16 && !T::HALF) return plane_of(v, col >= 8);
-    return v;
+  auto multiply = [](v4i x, v4i w, v4f sum) {
+    if constexpr (T::HALF) return mfma_h(x, w, sum);
+    return mfma_bf(x, w, sum);
   };
   // Half a chunk, `code`: the lane's scales.
   auto half = [&](const v4i (&wh)[RT], const uint32_t (&code)[RT], const v4i (&xh)[MT][STEPS]) {
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      v4i xf[MT];
-#pragma unroll
-      for (int t = 0; t < MT; ++t) xf[t] = operand(xh[t][s]);
+    for (int s = 0; s < STEPS; ++s)
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        if constexpr (T::HALF) {
-#pragma unroll
-          for (int t = 0; t < MT; ++t) acc[r][t] = mfma_h(xf[t], wh[r], acc[r][t]);
-        } else if constexpr (WK == W_H16) {
+        if constexpr (WK == W_H16 && !T::HALF) {
           v4i hi, lo;
           split_h(wh[r], hi, lo);
 #pragma unroll
-          for (int t = 0; t < MT; ++t) acc[r][t] = mfma_bf(xf[t], lo, mfma_bf(xf[t], hi, acc[r][t]));
+          for (int t = 0; t < MT; ++t) acc[r][t] = mfma_bf(xh[t][s], lo, mfma_bf(xh[t][s], hi, acc[r][t]));
         } else {
           v4i q = wh[r];
-          if constexpr (T::MX) q = decode<WK>(q, s, e8m0(code[r]));
+          if constexpr (T::MX) q = decode<WK, T::HALF>(q, s, S::decoding(code[r]));
 #pragma unroll
-          for (int t = 0; t < MT; ++t) acc[r][t] = mfma_bf(xf[t], q, acc[r][t]);
+          for (int t = 0; t < MT; ++t) acc[r][t] = multiply(xh[t][s], q, acc[r][t]);
         }
       }
-    }
   };
-  // The same under scales of which some may take an element out of bf16's normal
-  // numbers: each lane group's blocks by themselves, under a scale next to
-  // their own, and what that lacks applied to the sums.
+  // The same under any scales: each lane group's blocks by themselves, under a
+  // scale next to their own, and what that lacks applied to the sums.
   auto half_rare = [&](const v4i (&wh)[RT], const uint32_t (&code)[RT], const v4i (&xh)[MT][STEPS]) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
-        const float factor = lacking<WK>(static_cast<uint32_t>(__shfl(static_cast<int>(code[r]), 16 * q + col)));
+        const float factor = S::lacking(static_cast<uint32_t>(__shfl(static_cast<int>(code[r]), 16 * q + col)));
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           v4f alone = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int s = 0; s < STEPS; ++s) {
-            v4i v = decode<WK>(wh[r], s, e8m0(tame<WK>(code[r])));
-            if (g != q) v = v4i{0, 0, 0, 0};
-            alone = mfma_bf(operand(xh[t][s]), v, alone);
+            v4i v = decode<WK, T::HALF>(wh[r], s, S::decoding(S::tame(code[r])));
+            v4i u = xh[t][s];
+            if (g != q) u = v = v4i{0, 0, 0, 0};  // (an infinity, NaN may be in either)
+            alone = multiply(u, v, alone);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[r][t][e] += factor * alone[e];
@@ -322,7 +341,7 @@ __device__ __forceinline__ void products(const ExpertArgs& a, const uint8_t* con
   auto is_rare = [&](const uint32_t (&code)[RT]) {
     bool any = false;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) any |= code[r] != tame<WK>(code[r]);
+    for (int r = 0; r < RT; ++r) any |= code[r] != S::tame(code[r]);
     return __ballot(any) != 0;
   };
 
@@ -374,6 +393,13 @@ __device__ __forceinline__ void products(const ExpertArgs& a, const uint8_t* con
     }
   }
 
+  if constexpr (T::MX && S::SHIFT != 0) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) acc[r][t] *= exp2_of(127 - S::SHIFT);
+  }
+
   // The halves that were skipped, and K's partial chunk (whose number is
   // `whole`).  Loads that would pass a row's end end with it instead and are
   // shifted into place; rows shorter than a load go element by element.
@@ -416,7 +442,7 @@ __device__ __forceinline__ void products(const ExpertArgs& a, const uint8_t* con
       }
       bool rare = false;
       if constexpr (T::MX) {
-        rare = is_rare(code);
+        rare = is_rare(code) || (S::SHIFT != 0 && c == whole);
         if (rare) half_rare(wh, code, xh);
       }
       if (c == whole && !rare) half(wh, code, xh);
@@ -435,19 +461,13 @@ __device__ __forceinline__ void row_of(const ExpertArgs& a, int64_t expert, int 
   w = a.w + expert * a.w_expert + row * a.w_row;
   sf = WK == W_E4M3 || WK == W_E2M1 ? a.sf + expert * a.sf_expert + row * a.ld_sf : nullptr;
 }
-// The lane's row of activations: of choice `p`, or of its second plane.
-template <int WK, int XK>
-__device__ __forceinline__ const uint16_t* x_of(const ExpertArgs& a, int p, bool second) {
-  if constexpr (XK == X_PAIR) return (second ? a.lo : a.x) + static_cast<int64_t>(p) * a.ldx;
-  return a.x + static_cast<int64_t>(p / a.topk) * a.ldx;
-}
-
 // ---- the first product
-// A workgroup takes OUT tiles of features of one expert; its wavefronts split K.
-template <int WK, int XK, bool GATED, int OUT>
+// A workgroup takes sixteen features of one expert (and of a gated matrix what
+// their gates multiply); its wavefronts split K.
+template <int WK, int XK, bool GATED>
 __global__ void __launch_bounds__(64 * kWaves, 2) experts_up_kernel(ExpertArgs a) {
   using T = Kind<WK, XK>;
-  constexpr int RT = GATED ? 2 * OUT : OUT, MOST = 2, D = 2;
+  constexpr int RT = GATED ? 2 : 1, MOST = most_tiles(WK), D = 2;
   __shared__ int list[kMaxPairs];
   __shared__ int hits[2][kWaves];
   __shared__ float part[kWaves][RT][MOST][4][64];
@@ -463,12 +483,12 @@ __global__ void __launch_bounds__(64 * kWaves, 2) experts_up_kernel(ExpertArgs a
     expert = id_of(a, slot);
     live = expert >= 0 && expert < a.experts;
   }
-  const int f0 = static_cast<int>(blockIdx.x) * 16 * OUT;
+  const int f0 = static_cast<int>(blockIdx.x) * 16;
   const uint8_t* w[RT];
   const uint8_t* sf[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
-    row_of<WK>(a, live ? expert : 0, f0 + 16 * (r % OUT) + col, GATED && r >= OUT, w[r], sf[r]);
+    row_of<WK>(a, live ? expert : 0, f0 + col, r, w[r], sf[r]);
   Stream<WK, RT, D> st(a, wave, kWaves);
   // (of a choice that is not its expert's first these loads are for nothing)
   if (a.by_choice) st.start(a, w, sf);
@@ -509,8 +529,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2) experts_up_kernel(ExpertArgs a
     const uint16_t* x[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const int i = first + T::CAP * t + (T::PLANES ? col & 7 : col);
-      x[t] = x_of<WK, XK>(a, list[i < count ? i : count - 1], T::PLANES && col >= 8);
+      const int i = first + T::CAP * t + col;
+      x[t] = a.x + static_cast<int64_t>(list[i < count ? i : count - 1] / a.topk) * a.ldx;
     }
     v4f acc[RT][MT] = {};
     products<WK, XK, RT, MT, D>(a, w, sf, x, st, acc);
@@ -524,7 +544,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) experts_up_kernel(ExpertArgs a
   for (int first = 0; first < count;) {
     const int left = count - first, tiles = left > T::CAP ? MOST : 1;
     __syncthreads();  // the sums before these have been read
-    if (tiles == 1)
+    if (MOST == 1 || tiles == 1)
       run(first, std::integral_constant<int, 1>{});
     else
       run(first, std::integral_constant<int, MOST>{});
@@ -532,36 +552,30 @@ __global__ void __launch_bounds__(64 * kWaves, 2) experts_up_kernel(ExpertArgs a
     // Register e of lane l is choice 4 (l / 16) + e of the tile and feature l % 16.
     static_assert(kWaves == 4, "a wavefront finishes one register");
     for (int t = 0; t < tiles; ++t) {
-      const int row = 4 * g + wave, i = T::CAP * t + row;
-      if (row >= T::CAP || i >= left) continue;
+      const int i = T::CAP * t + 4 * g + wave;
+      if (i >= left) continue;
       auto sum = [&](int r) {
         float v = 0.0f;
 #pragma unroll
-        for (int q = 0; q < kWaves; ++q) {
-          v += part[q][r][t][wave][lane];
-          if constexpr (T::PLANES) v += part[q][r][t][wave][lane + 32];
-        }
+        for (int q = 0; q < kWaves; ++q) v += part[q][r][t][wave][lane];
         return v;
       };
       const int64_t at = list[first + i];
-#pragma unroll
-      for (int r = 0; r < OUT; ++r) {
-        const int f = f0 + 16 * r + col;
-        if (f >= a.features) continue;
-        const int64_t b = expert * a.bias_expert + f;
-        float v = sum(r);
-        if (a.bias) v += load_f(a.bias, a.bias_type, b);
-        v = activated(v, a.act);
-        if constexpr (GATED) {
-          float m = sum(OUT + r);
-          if (a.bias) m += load_f(a.bias, a.bias_type, b + a.features);
-          v *= m;
-        }
-        uint16_t hi, lo;
-        split_f(v, hi, lo);
-        a.u_hi[at * a.ld_u + f] = hi;
-        a.u_lo[at * a.ld_u + f] = lo;
+      const int f = f0 + col;
+      if (f >= a.features) continue;
+      const int64_t b = expert * a.bias_expert + f;
+      float v = sum(0);
+      if (a.bias) v += load_f(a.bias, a.bias_type, b);
+      v = activated(v, a.act);
+      if constexpr (GATED) {
+        float m = sum(1);
+        if (a.bias) m += load_f(a.bias, a.bias_type, b + a.features);
+        v *= m;
       }
+      uint16_t hi, lo;
+      split_f(v, hi, lo);
+      a.u_hi[at * a.ld_u + f] = hi;
+      a.u_lo[at * a.ld_u + f] = lo;
     }
     first += T::CAP * tiles;
     if (first < count) st.start(a, w, sf);
@@ -572,7 +586,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) experts_up_kernel(ExpertArgs a
 // The sums of an expert's choices over a wavefront's started stream, handed to
 // `put(place in `order`, choice, tile, feature of it, value)` by the lanes that hold
 // them, planes added.  At most MOST tiles of choices at a time.
-template <int WK, int RT, int D, class Put>
+template <int WK, int RT, int MOST, int D, class Put>
 __device__ __forceinline__ void down_choices(const ExpertArgs& a, const uint8_t* const (&w)[RT],
                                              const uint8_t* const (&sf)[RT], Stream<WK, RT, D>& st, const int* order,
                                              int count, Put put) {
@@ -584,7 +598,7 @@ __device__ __forceinline__ void down_choices(const ExpertArgs& a, const uint8_t*
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       const int i = first + T::CAP * t + (col & 7);
-      x[t] = x_of<WK, X_PAIR>(a, order[i < count ? i : count - 1], col >= 8);
+      x[t] = (col >= 8 ? a.lo : a.x) + static_cast<int64_t>(order[i < count ? i : count - 1]) * a.ldx;
     }
     v4f acc[RT][MT] = {};
     products<WK, X_PAIR, RT, MT, D>(a, w, sf, x, st, acc);
@@ -600,12 +614,12 @@ __device__ __forceinline__ void down_choices(const ExpertArgs& a, const uint8_t*
         }
   };
   for (int first = 0; first < count;) {
-    if (count - first <= T::CAP) {
+    if (MOST == 1 || count - first <= T::CAP) {
       run(first, std::integral_constant<int, 1>{});
       first += T::CAP;
     } else {
-      run(first, std::integral_constant<int, 2>{});
-      first += 2 * T::CAP;
+      run(first, std::integral_constant<int, MOST>{});
+      first += MOST * T::CAP;
     }
     if (first < count) st.start(a, w, sf);
   }
@@ -621,9 +635,9 @@ __device__ __forceinline__ void store_y(const ExpertArgs& a, int64_t j, int64_t 
     static_cast<__bf16*>(a.y)[to] = static_cast<__bf16>(v);
 }
 
-// Few slots: a workgroup takes sixteen features of every slot, its wavefronts
+// Few bytes: a workgroup takes sixteen features of every slot, its wavefronts
 // the slots (`ks` of them share one slot's K), and adds each token's choices.
-constexpr int kJoinWaves = 8;
+constexpr int kJoinWaves = 8, kJoinPairs = 64;
 
 template <int WK>
 __global__ void __launch_bounds__(64 * kJoinWaves, 2) experts_down_join_kernel(ExpertArgs a, int ks) {
@@ -656,7 +670,7 @@ __global__ void __launch_bounds__(64 * kJoinWaves, 2) experts_down_join_kernel(E
       copied = true;
     }
     if (s.count > 0)
-      down_choices<WK, 1, D>(a, w, sf, st, order + s.start, s.count,
+      down_choices<WK, 1, most_tiles(WK), D>(a, w, sf, st, order + s.start, s.count,
                              [&](int, int p, int, int f, float v) { mine[p * 16 + f] = v; });
   }
   __syncthreads();
@@ -680,11 +694,11 @@ __global__ void __launch_bounds__(64 * kJoinWaves, 2) experts_down_join_kernel(E
 // More of them: a workgroup takes RT tiles of features of one slot, its
 // wavefronts splitting K; z goes to the workspace, and a third launch adds
 // each token's choices.
-template <int WK, int RT>
+template <int WK>
 __global__ void __launch_bounds__(64 * kWaves, 2) experts_down_kernel(ExpertArgs a) {
   using T = Kind<WK, X_PAIR>;
-  constexpr int D = 2, MOST = 2 * T::CAP;
-  __shared__ float part[kWaves][MOST][16 * RT];
+  constexpr int RT = 2, D = 2, MOST = most_tiles(WK), ROWS = MOST * T::CAP;
+  __shared__ float part[kWaves][ROWS][16 * RT];
   const int tid = static_cast<int>(threadIdx.x), col = tid & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Slot slot = a.slots[blockIdx.y];
@@ -697,12 +711,12 @@ __global__ void __launch_bounds__(64 * kWaves, 2) experts_down_kernel(ExpertArgs
 #pragma unroll
   for (int r = 0; r < RT; ++r) row_of<WK>(a, slot.expert, f0 + 16 * r + col, 0, w[r], sf[r]);
   Stream<WK, RT, D> st(a, wave, kWaves);
-  for (int first = 0; first < count; first += MOST) {
+  for (int first = 0; first < count; first += ROWS) {
     st.start(a, w, sf);
-    const int left = count - first < MOST ? count - first : MOST;
+    const int left = count - first < ROWS ? count - first : ROWS;
     __syncthreads();  // the sums before these have been read
-    down_choices<WK, RT, D>(a, w, sf, st, order + first, left,
-                            [&](int i, int, int r, int f, float v) { part[wave][i][16 * r + f] = v; });
+    down_choices<WK, RT, MOST, D>(a, w, sf, st, order + first, left,
+                                  [&](int i, int, int r, int f, float v) { part[wave][i][16 * r + f] = v; });
     __syncthreads();
     for (int q = tid; q < left * 16 * RT; q += 64 * kWaves) {
       const int i = q / (16 * RT), f = q % (16 * RT);
@@ -748,7 +762,7 @@ template <int WK, int XK, bool GATED>
 hipError_t launch_up(ExpertArgs& a, hipStream_t st) {
   void* args[] = {&a};
   const int64_t tiles = (static_cast<int64_t>(a.features) + 15) / 16;
-  return hipLaunchKernel(reinterpret_cast<const void*>(&experts_up_kernel<WK, XK, GATED, 1>),
+  return hipLaunchKernel(reinterpret_cast<const void*>(&experts_up_kernel<WK, XK, GATED>),
                          dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(a.slot_count)), dim3(64 * kWaves),
                          args, 0, st);
 }
@@ -772,16 +786,25 @@ hipError_t launch_up(ExpertArgs& a, thl_dtype w, bool x_bf, bool gated, hipStrea
 template <int WK>
 hipError_t launch_down(ExpertArgs& a, hipStream_t st) {
   const int64_t tiles = (static_cast<int64_t>(a.features) + 15) / 16;
-  if (a.slot_count <= 16 && a.pairs <= 512) {
+  // Products and joining in one launch save a launch of 4.7 us, but every
+  // workgroup works through all slots.  One launch and two, of 4096 x 1024: eight
+  // slots of E2M1 9.4 and 13.8 us, sixteen of four choices each 21.9 and 24.2,
+  // thirty-two 25.9 and 27.0; eight of E4M3 13.3 and 18.6, twenty-four 30.2 and
+  // 30.7; two of bf16 7.4 and 9.4, eight 19.7 and 19.5, eight of eight choices
+  // each 27.7 and 21.8.  Of 2048 x 768: sixteen of E2M1 15.3 and 14.5, eight of
+  // E4M3 10.0 and 11.0, eight of bf16 14.2 and 11.9.  So by the bits of a weight
+  // of every slot.
+  constexpr int kBits = 128 / piece_of(WK);
+  if (a.slot_count * kBits <= 64 && a.pairs <= kJoinPairs) {
     int ks = 1;
-    while (2 * ks * a.slot_count <= kJoinWaves && 2 * ks * a.pairs <= 512) ks *= 2;
+    while (2 * ks * a.slot_count <= kJoinWaves) ks *= 2;
     void* args[] = {&a, &ks};
     return hipLaunchKernel(reinterpret_cast<const void*>(&experts_down_join_kernel<WK>),
                            dim3(static_cast<unsigned>(tiles)), dim3(64 * kJoinWaves), args,
                            static_cast<unsigned>(4 * a.pairs * (3 + 16 * ks)), st);
   }
   void* args[] = {&a};
-  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(&experts_down_kernel<WK, 2>),
+  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(&experts_down_kernel<WK>),
                                        dim3(static_cast<unsigned>((tiles + 1) / 2), static_cast<unsigned>(a.slot_count)),
                                        dim3(64 * kWaves), args, 0, st);
   if (e != hipSuccess) return e;
