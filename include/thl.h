@@ -589,7 +589,8 @@ thl_status thl_gemm_w4(int64_t m, int64_t n, int64_t k, const void* W, int64_t l
  *                 thl_moe_combine's and thl_moe_layer's.  A logit of -infinity or
  *                 NaN masks its expert, which then adds nothing to the softmax's
  *                 sum either; choices past the experts left get id -1, weight 0.
- *   bias          experts values for the choice alone (may be NULL)
+ *   bias          experts values for the choice alone (may be NULL); one of
+ *                 -infinity or NaN keeps its expert from being chosen
  * Computed in fp32.  Without a bias the logits themselves are compared.  A logit
  * of +infinity makes the softmax's weights NaN.  L in F32, F16 or BF16;
  * experts <= 1024, topk <= 64 (THL_ERR_UNSUPPORTED above).  No output may

@@ -105,6 +105,30 @@ def test_bias_for_the_choice(score, experts):
     assert not torch.equal(ids.cpu(), plain)  # the bias does choose
 
 
+def test_bias_that_chooses_far_below_the_largest():
+    # the chosen ones' softmax against the largest logit is nothing in fp32, their quotients are ordinary
+    l = _rand(3, 6, 200)
+    l[:, 7] = 300.0
+    bias = torch.zeros(200, device="cuda")
+    bias[[20, 90, 150]] = torch.tensor([6.0, 4.0, 2.0], device="cuda")
+    bias[7] = -1.5
+    ids, w = _run(l, 3, "softmax", True, bias=bias)
+    assert ids.tolist() == [[20, 90, 150]] * 6 and bool((w > 0).all())
+
+
+def test_bias_keeps_experts_from_being_chosen():
+    l = _rand(4, 5, 70)
+    bias = torch.zeros(70, device="cuda")
+    bias[2:60], bias[60:] = -torch.inf, float("nan")
+    for score in ("softmax", "sigmoid"):
+        ids = torch.empty(5, 4, dtype=torch.int32, device="cuda")
+        w = torch.empty(5, 4, device="cuda")
+        thl.moe_route(l, ids, w, score=score, renormalize=True, bias=bias)
+        torch.cuda.synchronize()
+        assert sorted(ids[0].tolist()) == [-1, -1, 0, 1] and ids[:, 2:].eq(-1).all() and w[:, 2:].eq(0).all()
+        assert bool((w.sum(dim=1) - 1).abs().max() <= 4 * ref.U)
+
+
 def test_many_tokens_and_pitched_rows():
     _run(_rand(0, 5000, 64), 4)
     n = (1 << 18) + 5  # more tokens than wavefronts of the grid

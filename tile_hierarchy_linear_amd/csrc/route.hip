@@ -238,7 +238,14 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
       const uint32_t other = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(its), t));
       rank += other > its || (other == its && t < lane);
     }
-    const float p = one ? (soft ? expf(v - top) / total : sigmoid(v)) : 0.0f;
+    // Divided by the chosen ones' sum, the softmax's may be shifted by the largest of
+    // them: with a bias that one can lie far below the largest of all.
+    float shift = top, of = total;
+    if (soft && a.renormalize && a.bias) {
+      const uint32_t most = wave_max(one ? key_of(v) : 0u);
+      shift = most ? value_of(most) : 0.0f, of = 1.0f;
+    }
+    const float p = one ? (soft ? expf(v - shift) / of : sigmoid(v)) : 0.0f;
     const float sum = a.renormalize ? wave_sum(p) : 1.0f;
     if (lane < a.topk) {
       const int64_t at = row * a.topk + (one ? rank : lane);
