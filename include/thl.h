@@ -637,8 +637,9 @@ thl_status thl_moe_route_backward(int64_t n, int64_t topk, int64_t experts, cons
  * Sums are fp32; u is kept with 16 significant bits (magnitudes above bf16's
  * largest, 3.39e38, count as infinite); Y rounds once.  A token that holds an
  * infinity or NaN gives infinities or NaN; other tokens do not see it.
- * n * topk <= 1024 (THL_ERR_UNSUPPORTED above): every 16 choices of an expert
- * stream its weights once more.
+ * n * topk <= 1024 (THL_ERR_UNSUPPORTED above): every 8 to 32 choices of an
+ * expert stream its weights once more.  experts * stride (of each stride) at
+ * most 2^40 (THL_ERR_UNSUPPORTED above).
  *   workspace  thl_moe_layer_workspace(m, hidden, n, topk) bytes, 4-byte aligned;
  *              not read before it is written, overlapping nothing.
  */

@@ -169,6 +169,8 @@ MX = dict(type="e2m1", sf=P[7])
     (dict(y=P[6]), INVALID), (dict(y=P[7], up=MX), INVALID), (dict(y=P[8], up=dict(bias=P[8], type_bias="f32")), INVALID),
     (dict(ws=P[0]), INVALID), (dict(ws=P[6]), INVALID), (dict(m=0), OK), (dict(n=0), OK),
     (dict(m=1 << 27, ldx=1 << 27, ldy=1 << 27), UNSUPPORTED), (dict(up=dict(stride=1 << 41)), UNSUPPORTED),
+    (dict(experts=1 << 30, up=dict(stride=1 << 33)), UNSUPPORTED),  # byte offsets past 64 bits
+    (dict(experts=1 << 30, up=MX, down=dict(MX, stride_sf=1 << 34)), UNSUPPORTED),
 ])
 def test_moe_layer_refusals(kw, want):
     assert layer(**kw) == want
