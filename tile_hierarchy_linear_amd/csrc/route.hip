@@ -17,8 +17,10 @@
 // bias the logits themselves are compared, exactly.
 //
 // Measured, 16,384 tokens' 8 of 256 experts, fp32 logits: 11.6 us, bound by
-// instructions (the logits' 17 MB take 3.3), and the gradient 10.8 us (34 MB: 6.7);
-// 16 tokens' 8 of 128 3.9 us, a launch.
+// instructions (the logits' 17 MB take 3.3), and the gradient of sigmoid scores
+// 8.5 us (its 17 MB and the chosen logits' lines: 5), of softmax ones 13.0 (34 MB:
+// 6.7), instructions too: with every choice's value offered to every lane 12.1
+// and 15.7.  16 tokens' 8 of 128 3.9 us, a launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -98,6 +100,14 @@ __device__ __forceinline__ uint32_t extent(uint32_t v, int k, uint32_t& least) {
   const v2u a = __builtin_amdgcn_permlane16_swap(v, v, false, false), b = __builtin_amdgcn_permlane16_swap(low, low, false, false);
   least = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(min(b[0], b[1]))));
   return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(max(a[0], a[1]))));
+}
+
+// Between a wavefront's writes to LDS and its other lanes' reads of them: its
+// accesses run in order, so this holds back the compiler alone.
+__device__ __forceinline__ void lds_exchange() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // The bits of `mask` below this lane's.
@@ -213,7 +223,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
     }
     __shared__ uint32_t chosen[4][3][64];  // keys, experts, logits
     uint32_t(&mine)[3][64] = chosen[threadIdx.x >> 6];
-    __builtin_amdgcn_wave_barrier();  // a wavefront's LDS accesses run in order
+    lds_exchange();
     int place = 0, same = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -228,7 +238,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
       if (in) mine[0][at] = key[i], mine[1][at] = 64 * i + lane, mine[2][at] = __builtin_bit_cast(uint32_t, l[i]);
       place += __popcll(who);
     }
-    __builtin_amdgcn_wave_barrier();
+    lds_exchange();
     const bool one = lane < k;  // this lane's choice
     const uint32_t its = mine[0][lane];
     const int id = static_cast<int>(mine[1][lane]);
@@ -261,6 +271,8 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
 // the sigmoid.
 template <int PER>
 __global__ void __launch_bounds__(256) route_grad_kernel(RouteArgs a) {
+  __shared__ int values[4][64 * PER];
+  int(&mine)[64 * PER] = values[threadIdx.x >> 6];
   const int lane = static_cast<int>(threadIdx.x) & 63;
   const int64_t waves = static_cast<int64_t>(gridDim.x) * 4;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); row < a.n; row += waves) {
@@ -309,13 +321,31 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteArgs a) {
 #pragma unroll
     for (int i = 0; i < PER; ++i)
       o[i] = all && l[i] > -INFINITY ? -a.scale * mean * (expf(l[i] - top) / total) : 0.0f;
-    for (int t = 0; t < a.topk; ++t) {  // in the order of the choices
-      const int e = __builtin_amdgcn_readlane(id, t);
-      const float dt = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, d), t));
-      const float to = (e & 63) == lane ? dt : 0.0f;
+    // The choices' values reach their experts' lanes through LDS.  A lane number
+    // there first tells whether two choices share an expert; those are added one
+    // by one, in their order.
+    lds_exchange();
 #pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (e >> 6 == i) o[i] += to;
+    for (int i = 0; i < PER; ++i) mine[64 * i + lane] = 0;
+    lds_exchange();
+    if (id >= 0) mine[id] = lane;
+    lds_exchange();
+    const bool twice = __ballot(id >= 0 && mine[id >= 0 ? id : 0] != lane) != 0;
+    lds_exchange();
+    if (!twice) {
+      if (id >= 0) mine[id] = __builtin_bit_cast(int, d);
+      lds_exchange();
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[i] += __builtin_bit_cast(float, mine[64 * i + lane]);
+    } else {
+      for (int t = 0; t < a.topk; ++t) {
+        const int e = __builtin_amdgcn_readlane(id, t);
+        const float dt = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, d), t));
+        const float to = (e & 63) == lane ? dt : 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (e >> 6 == i) o[i] += to;
+      }
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
