@@ -210,6 +210,27 @@ def test_gradient_of_the_same_expert_twice_and_of_none(score, renorm):
     assert bool((dl == 0).all())
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("n,experts,topk", [(4099, 60, 16), (4099, 64, 17), (8195, 100, 5), (16385, 200, 8)])
+def test_gradient_of_many_tokens(score, n, experts, topk):
+    # few experts, many tokens: several tokens a wavefront; some choices shared, some of no expert
+    g = torch.Generator().manual_seed(n)
+    l = _rand(n, n, experts)
+    ids = torch.stack([torch.randperm(experts, generator=g)[:topk] for _ in range(n)]).int()
+    ids[5::9, 1] = ids[5::9, 0]
+    ids[2::7, -1] = -1
+    ids[n - 1] = experts
+    dw = torch.randn(n, topk, generator=g)
+    dl = torch.full_like(l, float("nan"))
+    thl.moe_route_backward(l, ids.cuda(), dw.cuda(), dl, score=score, renormalize=True, scale=1.5)
+    torch.cuda.synchronize()
+    want = ref.moe_route_backward(l, ids, dw, score, True, 1.5)
+    # each choice's w (g - along), with |along| <= max|g| and w <= 1: REL of w, of along and (sigmoid) of the slope, of
+    # magnitudes up to 2 max|g|; two choices at most in one place
+    near = 10 * REL * 1.5 * dw.abs().amax(dim=1, keepdim=True).double()
+    assert bool(((ref.f64(dl) - want).abs() <= near).all())
+
+
 def test_gradient_against_differences():
     """Central differences of the fp64 weights in a random direction: off by h^2 / 6 of a third derivative of order one."""
     l = _rand(3, 6, 40)

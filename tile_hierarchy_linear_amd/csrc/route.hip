@@ -18,7 +18,7 @@
 //
 // Measured, 16,384 tokens' 8 of 256 experts, fp32 logits: 11.6 us, bound by
 // instructions (the logits' 17 MB take 3.3), and the gradient of sigmoid scores
-// 8.5 us (its 17 MB and the chosen logits' lines: 5), of softmax ones 13.0 (34 MB:
+// 7.7 us (its 17 MB and the chosen logits' lines: 5), of softmax ones 10.9 (34 MB:
 // 6.7), instructions too: with every choice's value offered to every lane 12.1
 // and 15.7.  16 tokens' 8 of 128 3.9 us, a launch.
 #include <hip/hip_runtime.h>
@@ -67,11 +67,15 @@ template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
   return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xf, 0xf, true)));
 }
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+// (over the sixteen lanes of a row)
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
   v = dpp_max<0xb1>(v);
   v = dpp_max<0x4e>(v);
   v = dpp_max<0x141>(v);
-  v = dpp_max<0x140>(v);
+  return dpp_max<0x140>(v);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max16(v);
   const v2u h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   v = max(h[0], h[1]);
   const v2u a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
@@ -155,13 +159,16 @@ __device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t row, int
   for (int i = 0; i < PER; ++i) l[i] = 64 * i + lane < a.experts ? l[i] : -INFINITY;
 }
 
-// The largest logit that is a number above -infinity (the shift of the
-// softmax), and the sum of the exponentials.
+// The logits' exponentials under `top`, the largest one that is a number above
+// -infinity, in their place (0 for one that is masked), and their sum.
 template <int PER>
-__device__ __forceinline__ float softmax_sum(const float (&l)[PER], float top) {
+__device__ __forceinline__ float softmax_sum(float (&l)[PER], float top) {
   float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) s += l[i] > -INFINITY ? expf(l[i] - top) : 0.0f;
+  for (int i = 0; i < PER; ++i) {
+    l[i] = l[i] > -INFINITY ? expf(l[i] - top) : 0.0f;
+    s += l[i];
+  }
   return wave_sum(s);
 }
 
@@ -183,12 +190,15 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
     const bool soft = a.score == THL_ROUTE_SOFTMAX;
     const float top = best ? value_of(best) : 0.0f;
     // with the chosen ones' sum alone in the quotient, the others' is not needed
-    const float total = soft && (a.bias || !a.renormalize) ? softmax_sum<PER>(l, top) : 1.0f;
+    float x[PER], total = 1.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) x[i] = l[i];
+    if (soft && (a.bias || !a.renormalize)) total = softmax_sum<PER>(x, top);
     if (a.bias) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int e = 64 * i + lane;
-        const float p = soft ? expf(l[i] - top) / total : sigmoid(l[i]);
+        const float p = soft ? x[i] / total : sigmoid(l[i]);
         key[i] = key[i] && e < a.experts ? key_of(p + a.bias[e]) : 0u;
       }
     }
@@ -269,105 +279,132 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
 // gradient g_t of w_t, d p_t = scale * (g_t - sum_c g_c p_c / P) / P, or scale * g_t;
 // then d l = p (d p - sum_e p_e d p_e) for the softmax and d p * p (1 - p) for
 // the sigmoid.
-template <int PER>
+//
+// A wavefront takes 64 / G tokens, G lanes the choices of one: with G = 16 only
+// where the choices alone have a gradient.
+template <int PER, int G>
 __global__ void __launch_bounds__(256) route_grad_kernel(RouteArgs a) {
-  __shared__ int values[4][64 * PER];
-  int(&mine)[64 * PER] = values[threadIdx.x >> 6];
-  const int lane = static_cast<int>(threadIdx.x) & 63;
-  const int64_t waves = static_cast<int64_t>(gridDim.x) * 4;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); row < a.n; row += waves) {
-    const bool soft = a.score == THL_ROUTE_SOFTMAX;
+  constexpr int TOKENS = 64 / G;
+  __shared__ int values[4][TOKENS][64 * PER];
+  int(&mine)[TOKENS][64 * PER] = values[threadIdx.x >> 6];
+  const int lane = static_cast<int>(threadIdx.x) & 63, sub = lane & (G - 1);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 4 * TOKENS;
+  const bool soft = a.score == THL_ROUTE_SOFTMAX;
+  const bool all = G == 64 && soft && !a.renormalize;  // the other experts have a gradient
+  auto sum_of = [](float v) { return G == 64 ? wave_sum(v) : sum16(v); };
+  auto max_of = [](uint32_t v) { return G == 64 ? wave_max(v) : max16(v); };
+#pragma unroll
+  for (int j = 0; j < TOKENS; ++j)
+#pragma unroll
+    for (int i = 0; i < PER; ++i) mine[j][64 * i + lane] = 0;
+  for (int64_t row0 = (static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6)) * TOKENS; row0 < a.n; row0 += step) {
+    const int64_t its = row0 + lane / G;
     int id = -1;
     float g = 0.0f, v = -INFINITY;
-    if (lane < a.topk) {
-      id = a.ids[row * a.topk + lane];
+    if (sub < a.topk && its < a.n) {
+      id = a.ids[its * a.topk + sub];
       if (id < 0 || id >= a.experts) {
         id = -1;
       } else {
-        g = a.dweights[row * a.topk + lane];
-        v = load_f(a.logits, a.type, row * a.ld + id);
+        g = a.dweights[its * a.topk + sub];
+        v = load_f(a.logits, a.type, its * a.ld + id);
       }
     }
-    float l[PER], top = 0.0f, total = 1.0f;
-    const bool all = soft && !a.renormalize;  // the other experts have a gradient
-    if (all) load_logits<PER>(a, row, lane, l);
+    float o[PER] = {}, top = 0.0f, total = 1.0f;
+    if (all) load_logits<PER>(a, row0, lane, o);
     if (soft) {
       uint32_t best = key_of(v);
       if (all) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) best = max(best, key_of(l[i]));
+        for (int i = 0; i < PER; ++i) best = max(best, key_of(o[i]));
       }
-      best = wave_max(best);
+      best = max_of(best);
       top = best ? value_of(best) : 0.0f;
-      if (all) total = softmax_sum<PER>(l, top);
+      if (all) total = softmax_sum<PER>(o, top);
     }
     const float p = id < 0 ? 0.0f : (soft ? expf(v - top) / total : sigmoid(v));
-    const float sum = a.renormalize ? wave_sum(p) : 1.0f;
-    float d = 0.0f, mean = 0.0f;  // d l of this choice, less what all experts share
+    const float sum = a.renormalize ? sum_of(p) : 1.0f;
+    float d = 0.0f;  // d l of this choice, less what all experts share
     if (a.renormalize) {
-      const float w = sum == 0.0f ? 0.0f : p / sum, along = wave_sum(w * g);
+      const float w = sum == 0.0f ? 0.0f : p / sum, along = sum_of(w * g);
       if (soft)
         d = w * (g - along);
       else
         d = sum == 0.0f ? 0.0f : w * (g - along) * sigmoid(-v);
     } else if (soft) {
-      mean = wave_sum(p * g);
+      const float shared = -a.scale * wave_sum(p * g) / total;
       d = p * g;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[i] = o[i] != 0.0f ? shared * o[i] : 0.0f;  // (a masked one has none)
     } else {
       d = p * g * sigmoid(-v);
     }
     d = id < 0 ? 0.0f : a.scale * d;
-    float o[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      o[i] = all && l[i] > -INFINITY ? -a.scale * mean * (expf(l[i] - top) / total) : 0.0f;
-    // The choices' values reach their experts' lanes through LDS.  A lane number
-    // there first tells whether two choices share an expert; those are added one
-    // by one, in their order.
+    // The choices' values reach their experts' lanes through LDS, which is zero
+    // before and after.  A lane number there first tells whether two choices of
+    // a token share an expert; such are added one by one, in their order.
+    int* const place = &mine[TOKENS > 1 ? lane / G : 0][id < 0 ? 0 : id];
+    lds_exchange();
+    if (id >= 0) *place = lane;
+    lds_exchange();
+    const bool twice = __ballot(id >= 0 && *place != lane) != 0;
+    lds_exchange();
+    if (id >= 0) *place = twice ? 0 : __builtin_bit_cast(int, d);
     lds_exchange();
 #pragma unroll
-    for (int i = 0; i < PER; ++i) mine[64 * i + lane] = 0;
-    lds_exchange();
-    if (id >= 0) mine[id] = lane;
-    lds_exchange();
-    const bool twice = __ballot(id >= 0 && mine[id >= 0 ? id : 0] != lane) != 0;
-    lds_exchange();
-    if (!twice) {
-      if (id >= 0) mine[id] = __builtin_bit_cast(int, d);
-      lds_exchange();
+    for (int j = 0; j < TOKENS; ++j) {
+      const int64_t row = row0 + j;
+      if (row >= a.n) break;
+      float to[PER];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) o[i] += __builtin_bit_cast(float, mine[64 * i + lane]);
-    } else {
-      for (int t = 0; t < a.topk; ++t) {
-        const int e = __builtin_amdgcn_readlane(id, t);
-        const float dt = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, d), t));
-        const float to = (e & 63) == lane ? dt : 0.0f;
+      for (int i = 0; i < PER; ++i) to[i] = o[i] + __builtin_bit_cast(float, mine[j][64 * i + lane]);
+      if (twice) {
+        for (int t = 0; t < a.topk; ++t) {
+          const int e = __builtin_amdgcn_readlane(id, G * j + t);
+          const float dt = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, d), G * j + t));
+          const float one = (e & 63) == lane ? dt : 0.0f;
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-          if (e >> 6 == i) o[i] += to;
+          for (int i = 0; i < PER; ++i)
+            if (e >> 6 == i) to[i] += one;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int e = 64 * i + lane;
+        if (e >= a.experts) continue;
+        const int64_t at = row * a.ldd + e;
+        if (a.type == THL_F32)
+          static_cast<float*>(a.dlogits)[at] = to[i];
+        else if (a.type == THL_F16)
+          static_cast<_Float16*>(a.dlogits)[at] = static_cast<_Float16>(to[i]);
+        else
+          static_cast<__bf16*>(a.dlogits)[at] = static_cast<__bf16>(to[i]);
       }
     }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = 64 * i + lane;
-      if (e >= a.experts) continue;
-      const int64_t at = row * a.ldd + e;
-      if (a.type == THL_F32)
-        static_cast<float*>(a.dlogits)[at] = o[i];
-      else if (a.type == THL_F16)
-        static_cast<_Float16*>(a.dlogits)[at] = static_cast<_Float16>(o[i]);
-      else
-        static_cast<__bf16*>(a.dlogits)[at] = static_cast<__bf16>(o[i]);
-    }
+    lds_exchange();
+    if (id >= 0) *place = 0;
   }
 }
 
 template <int PER>
 hipError_t launch(RouteArgs& a, hipStream_t st) {
-  const void* f = a.dlogits ? reinterpret_cast<const void*>(&route_grad_kernel<PER>)
-                            : reinterpret_cast<const void*>(&route_kernel<PER>);
+  const void* f = reinterpret_cast<const void*>(&route_kernel<PER>);
+  int64_t tokens = 4;  // of a workgroup
+  if (a.dlogits) {
+    f = reinterpret_cast<const void*>(&route_grad_kernel<PER, 64>);
+    // Four tokens a wavefront, where there are tokens for it: sigmoid scores of 64,
+    // 128 and 256 experts, 32,768 tokens 6.3, 8.6 and 11.3 us, 10.8, 11.5 and 14.0
+    // one a wavefront; 4,096 tokens 3.2, 3.8 and 4.9 us, 3.3, 3.6 and 4.3.  512
+    // experts: 24.0 for 22.8.
+    if constexpr (PER <= 4) {
+      if (a.topk <= 16 && (a.score != THL_ROUTE_SOFTMAX || a.renormalize) && a.n >= 4096 * PER) {
+        f = reinterpret_cast<const void*>(&route_grad_kernel<PER, 16>);
+        tokens = 16;
+      }
+    }
+  }
   void* args[] = {&a};
-  const int64_t blocks = (a.n + 3) / 4;
+  const int64_t blocks = (a.n + tokens - 1) / tokens;
   return hipLaunchKernel(f, dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536)), dim3(256), args, 0, st);
 }
 hipError_t launch(RouteArgs& a, hipStream_t st) {
