@@ -15,7 +15,7 @@
 // a time under their scale by the hardware's instruction.
 //
 // Measured: 2,048 x 8,192 bf16 values to E2M1 10.0 us (4.2 TB/s), 8,192 x 8,192
-// both ways 51 us (4.0 TB/s; a large copy runs at 5.0), 1,531 x 5,003 fp32 values
+// both ways 48 us (4.3 TB/s; a large copy runs at 5.0), 1,531 x 5,003 fp32 values
 // to E4M3 8.5 us (4.5 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(256) mx_rows_kernel(MxArgs a) {
   }
 }
 
-constexpr int kTile = 128;
+constexpr int kTile = 128, kPanel = 8;
 
 // Blocks along the tokens, and along the features if y is given: a tile of 128 x
 // 128 values.  16 lanes hold a row's 128 features; behind LDS a lane holds
@@ -261,12 +261,18 @@ __global__ void __launch_bounds__(256) mx_turn_kernel(MxArgs a) {
   __shared__ __attribute__((aligned(16))) uint32_t tile[kTile * ROW];
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wave = tid >> 6;
   const int64_t tiles_m = (static_cast<int64_t>(a.m) + kTile - 1) / kTile, tiles_n = (a.n + kTile - 1) / kTile;
-  // Tiles next to one another along the tokens share lines of yt: a stretch of
-  // them to each XCD (workgroups go round the eight), 51 us for 56.
+  // Tiles next to one another share lines of yt along the tokens, and along the
+  // features lines of y and of the scales (four bytes of a tile's row): to each
+  // XCD a stretch of them (workgroups go round the eight), in panels of kPanel
+  // tiles of features.  8,192 x 8,192 bf16 to E2M1 56 us in the workgroups' order,
+  // 51 with stretches along the tokens, 48 with panels; 4,096 x 8,192 fp32 48 and
+  // 43 with panels.
   const int64_t tiles = tiles_m * tiles_n, stretch = tiles / 8;
   for (int64_t u0 = blockIdx.x; u0 < tiles; u0 += gridDim.x) {
     const int64_t u = u0 < 8 * stretch ? (u0 & 7) * stretch + (u0 >> 3) : u0;
-    const int64_t tm = u / tiles_n, tn = u - tm * tiles_n;
+    const int64_t panel = u / (kPanel * tiles_n), in = u - panel * kPanel * tiles_n;
+    const int64_t wide = tiles_m - panel * kPanel < kPanel ? tiles_m - panel * kPanel : kPanel;
+    const int64_t tn = in / wide, tm = panel * kPanel + in - tn * wide;
     const int64_t row0 = kTile * tn + (tid >> 4);
     const int e = static_cast<int>(tm) * kTile + 8 * (tid & 15), there = e < a.m ? a.m - e : 0;
     Run<X> r[8];
