@@ -16,7 +16,7 @@
 // 8 of 256 experts.)  Softmax and sigmoid keep the logits' order, so without a
 // bias the logits themselves are compared, exactly.
 //
-// Measured, 16,384 tokens' 8 of 256 experts, fp32 logits: 11.6 us, bound by
+// Measured, 16,384 tokens' 8 of 256 experts, fp32 logits: 11.3 us, bound by
 // instructions (the logits' 17 MB take 3.3), and the gradient of sigmoid scores
 // 7.7 us (its 17 MB and the chosen logits' lines: 5), of softmax ones 10.9 (34 MB:
 // 6.7), instructions too: with every choice's value offered to every lane 12.1
@@ -250,13 +250,20 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
     }
     lds_exchange();
     const bool one = lane < k;  // this lane's choice
-    const uint32_t its = mine[0][lane];
     const int id = static_cast<int>(mine[1][lane]);
     const float v = __builtin_bit_cast(float, mine[2][lane]);
-    int rank = 0;
-    for (int t = 0; t < k; ++t) {
-      const uint32_t other = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(its), t));
-      rank += other > its || (other == its && t < lane);
+    int rank = 0;  // the chosen ones before it
+    if (k <= 8) {  // every pair of them in one comparison: byte t is choice t's
+      const int t = lane >> 3, o = lane & 7;
+      const uint32_t a = mine[0][t], b = mine[0][o];
+      const uint64_t before = __ballot(o < k && (b > a || (b == a && o < t)));
+      rank = __popc(static_cast<uint32_t>(before >> (8 * o)) & 255u);
+    } else {
+      const uint32_t its = mine[0][lane];
+      for (int t = 0; t < k; ++t) {
+        const uint32_t other = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(its), t));
+        rank += other > its || (other == its && t < lane);
+      }
     }
     // Divided by the chosen ones' sum, the softmax's may be shifted by the largest of
     // them: with a bias that one can lie far below the largest of all.
