@@ -161,11 +161,11 @@ __device__ __forceinline__ float exp2_of(uint32_t e) { return __builtin_bit_cast
 // MX blocks are decoded with 2^SHIFT times their scale, and the sums divided by
 // it.  An E8M0 code b = LO .. HI so makes every element a number of the type:
 // a normal bf16 number, or an fp16 number (of E4M3, down to its subnormal ones).
-// With SHIFT the 23 to 27 powers of two that fp16 has room for lie where
-// weights' scales do: maxima from 2^-15 to 2^8 or 2^-17 to 2^10.
+// With SHIFT the 23 or 27 powers of two that fp16 has room for lie where
+// weights' scales do: 2^-21 to 2^1, or 2^-19 to 2^7 of E2M1.
 template <int WK, bool H>
 struct Scales {
-  static constexpr int SHIFT = !H ? 0 : (WK == W_E2M1 ? 6 : 8);
+  static constexpr int SHIFT = H ? 6 : 0;
   static constexpr uint32_t LO = !H ? (WK == W_E2M1 ? 2 : 10) : (WK == W_E2M1 ? 127 - 13 - SHIFT : 127 - 15 - SHIFT);
   static constexpr uint32_t HI = !H ? (WK == W_E2M1 ? 252 : 246) : (WK == W_E2M1 ? 127 + 13 - SHIFT : 127 + 7 - SHIFT);
   // The code next to b in that range, and what a sum decoded under it lacks.
