@@ -238,6 +238,14 @@ def test_backward_more_tokens_than_workgroups(n, m, g):
     _grad(n, m, s="f32" if g == "f32" else "bf16", g=g, seed=n, dres=g == "f32")
 
 
+@pytest.mark.parametrize("s", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("g", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("m", [8200, 12291])
+def test_backward_of_long_tokens(s, g, m):
+    # two runs a lane on sixteen wavefronts, several tokens a workgroup
+    _grad(520, m, s=s, g=g, seed=m, dres=True)
+
+
 def test_backward_with_a_mean_far_from_zero():
     for m in (300, 8192, 16400):
         _grad(30, m, s="f32", g="f32", shift=300.0)

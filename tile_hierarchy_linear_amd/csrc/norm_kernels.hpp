@@ -391,6 +391,10 @@ __global__ void __launch_bounds__(WPR * tokens_at_once(WPR) * 64) norm_grad_kern
     // 4,096 bf16 with dr 58 us for 66.  Two runs a lane on sixteen wavefronts
     // have no registers for it.
     constexpr bool AHEAD = CENTRED && WPR <= 8;
+    // Those hold 16-bit runs as loaded across the sums and convert them again
+    // after each: in fp32 they spill 100 registers.  2,048 x 12,288 bf16 58 us for
+    // 88, fp32 with bf16 gradients 72 for 85; bf16 with fp32 gradients 97 for 89.
+    constexpr bool AGAIN = CENTRED && WPR == 16 && GB == 2;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * TOKENS + which;
     Raw8<SB> sn[AHEAD ? NC : 1];
     Raw8<GB> gn[AHEAD ? NC : 1], rn[AHEAD ? NC : 1];
@@ -405,7 +409,7 @@ __global__ void __launch_bounds__(WPR * tokens_at_once(WPR) * 64) norm_grad_kern
       } else {
         load_row(row, sr, gr, rr);
       }
-      float s[NC][8], g[NC][8], sum[NS] = {};
+      float s[NC][8], g[NC][8], sum[NS] = {}, mu = 0.0f;
       if constexpr (CENTRED) {
         float total[1] = {0.0f};
 #pragma unroll
@@ -416,9 +420,15 @@ __global__ void __launch_bounds__(WPR * tokens_at_once(WPR) * 64) norm_grad_kern
           for (int i = 0; i < 8; ++i) total[0] += s[c][i];
         }
         row_sum<1, WPR>(total, red_mean);
-        const float mu = total[0] / static_cast<float>(m);
+        mu = total[0] / static_cast<float>(m);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) centre<RUNS>(s[c], mu, 8 * (t + T * c), m);
+        for (int c = 0; c < NC; ++c) {
+          if constexpr (AGAIN) {
+            arrived(sr[c]);
+            to_f8<SB>(sr[c], s_bf, s[c]);
+          }
+          centre<RUNS>(s[c], mu, 8 * (t + T * c), m);
+        }
       }
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
@@ -449,6 +459,12 @@ __global__ void __launch_bounds__(WPR * tokens_at_once(WPR) * 64) norm_grad_kern
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         float d[8] = {}, h[8];
+        if constexpr (AGAIN) {
+          arrived(sr[c]), arrived(gr[c]), arrived(rr[c]);
+          to_f8<SB>(sr[c], s_bf, s[c]);
+          centre<RUNS>(s[c], mu, 8 * (t + T * c), m);
+          to_f8<GB>(gr[c], g_bf, g[c]);
+        }
         if (a.dr) to_f8<GB>(rr[c], g_bf, d);
         emit(row, 8 * (t + T * c), s[c], g[c], w[c], d, rho, mean, level, h);
         if constexpr (IN_LDS) {

@@ -16,7 +16,7 @@
 // 8 of 256 experts.)  Softmax and sigmoid keep the logits' order, so without a
 // bias the logits themselves are compared, exactly.
 //
-// Measured, 16,384 tokens' 8 of 256 experts, fp32 logits: 11.3 us, bound by
+// Measured, 16,384 tokens' 8 of 256 experts, fp32 logits: 11 us, bound by
 // instructions (the logits' 17 MB take 3.3), and the gradient of sigmoid scores
 // 7.7 us (its 17 MB and the chosen logits' lines: 5), of softmax ones 10.9 (34 MB:
 // 6.7), instructions too: with every choice's value offered to every lane 12.1
