@@ -12,6 +12,13 @@ F = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16, "e4m3":
 EPS = 1e-5
 
 
+@pytest.fixture(scope="module", autouse=True)
+def _give_back():
+    """What lives on (a library's workspace, say) is not cut from these tests' large blocks."""
+    yield
+    torch.cuda.empty_cache()
+
+
 @pytest.fixture(autouse=True)
 def _gpu():
     if not torch.cuda.is_available():

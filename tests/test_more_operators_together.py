@@ -11,6 +11,13 @@ pytestmark = pytest.mark.gpu
 EPS = 1e-5
 
 
+@pytest.fixture(scope="module", autouse=True)
+def _give_back():
+    """What lives on (a library's workspace, say) is not cut from these tests' large blocks."""
+    yield
+    torch.cuda.empty_cache()
+
+
 @pytest.fixture(autouse=True)
 def _gpu():
     if not torch.cuda.is_available():

@@ -13,6 +13,13 @@ F = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 REL = (30 + 22 + 12) * ref.U
 
 
+@pytest.fixture(scope="module", autouse=True)
+def _give_back():
+    """What lives on (a library's workspace, say) is not cut from these tests' large blocks."""
+    yield
+    torch.cuda.empty_cache()
+
+
 @pytest.fixture(autouse=True)
 def _gpu():
     if not torch.cuda.is_available():
