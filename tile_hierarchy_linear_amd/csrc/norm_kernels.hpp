@@ -387,13 +387,17 @@ __global__ void __launch_bounds__(WPR * tokens_at_once(WPR) * 64) norm_grad_kern
       }
     };
     // Centred, with a second sum across the workgroup, a token waits long enough
-    // to ask for the next one first (the last one asks for itself again): 8,192 x
-    // 4,096 bf16 with dr 58 us for 66.  Two runs a lane on sixteen wavefronts
-    // have no registers for it.
-    constexpr bool AHEAD = CENTRED && WPR <= 8;
-    // Those hold 16-bit runs as loaded across the sums and convert them again
-    // after each: in fp32 they spill 100 registers.  2,048 x 12,288 bf16 58 us for
-    // 88, fp32 with bf16 gradients 72 for 85; bf16 with fp32 gradients 97 for 89.
+    // to ask for the next one first (the last one asks for itself again): with dr
+    // 8,192 x 4,096 bf16 58 us for 66, 16,384 x 2,048 54 for 56 (fp32 108 for 111),
+    // x 1,024 31 for 32.  Not on one wavefront, nor fp32 on two, which have others
+    // to wait beside: 20,000 x 500 fp32 46 for 37, 16,384 x 1,001 66 for 62.  Nor two
+    // runs a lane, whose registers then leave one workgroup a CU: 8,192 x 6,144 bf16
+    // 105 for 85, 2,048 x 8,192 fp32 71 for 60.
+    constexpr bool AHEAD = CENTRED && NC == 1 && SB + 2 * GB <= 3 * WPR;
+    // On sixteen wavefronts two 16-bit runs stay as loaded across the sums and are
+    // converted again after each: in fp32 they spill 100 registers.  2,048 x 12,288
+    // bf16 58 us for 88, fp32 with bf16 gradients 72 for 85; bf16 with fp32
+    // gradients 97 for 89.
     constexpr bool AGAIN = CENTRED && WPR == 16 && GB == 2;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * TOKENS + which;
     Raw8<SB> sn[AHEAD ? NC : 1];
