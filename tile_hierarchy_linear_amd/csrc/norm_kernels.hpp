@@ -635,9 +635,12 @@ hipError_t launch(const void* f, int64_t grid, int block, void* arg, hipStream_t
 }
 
 // Workgroups: one per token up to what keeps the device full several times
-// over; each then walks its tokens.
-int64_t norm_grid(int64_t n, int wpr) {
-  const int64_t most = 32768 / wpr;
+// over; each then walks its tokens.  Weights and biases, which a workgroup loads
+// once, want a quarter as many: with residual and its sum, bf16, 8,192 x 5,003 86 us
+// for 106, 4,096 x 12,288 94 for 101, 65,536 x 256 37 for 43, 1,024 x 8,192 19.5 for
+// 21.7; but from 1,025 to 4,096 features, 16,384 x 4,096 98 for 93.
+int64_t norm_grid(bool centred, int64_t m, int64_t n, int wpr) {
+  const int64_t most = (centred && (m <= 1024 || m > 4096) ? 8192 : 32768) / wpr;
   return n < most ? n : most;
 }
 
@@ -647,8 +650,8 @@ int64_t norm_grid(int64_t n, int wpr) {
 template <bool CENTRED, int XB, int RB, int RUNS>
 hipError_t launch_norm(NormArgs& a, hipStream_t st) {
 #define THL_NORM(WPR, CH)                                                                                            \
-  return launch(reinterpret_cast<const void*>(&norm_kernel<CENTRED, XB, RB, WPR, CH, RUNS>), norm_grid(a.n, WPR), \
-                WPR * 64, &a, st)
+  return launch(reinterpret_cast<const void*>(&norm_kernel<CENTRED, XB, RB, WPR, CH, RUNS>),                         \
+                norm_grid(CENTRED, a.m, a.n, WPR), WPR * 64, &a, st)
   const bool few = a.n <= 1024;
   if (a.m <= 512) THL_NORM(1, 1);
   if constexpr (RUNS != RUNS_TINY) {
