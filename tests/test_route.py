@@ -236,6 +236,9 @@ def test_gradient_of_many_tokens(score, n, experts, topk):
     # magnitudes up to 2 max|g|; two choices at most in one place
     near = 10 * REL * 1.5 * dw.abs().amax(dim=1, keepdim=True).double()
     assert bool(((ref.f64(dl) - want).abs() <= near).all())
+    thl.moe_route_backward(l, ids.cuda(), dw.cuda(), l, score=score, renormalize=True, scale=1.5)  # in place
+    torch.cuda.synchronize()
+    assert torch.equal(l, dl)
 
 
 def test_gradient_against_differences():
