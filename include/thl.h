@@ -634,8 +634,7 @@ thl_status thl_moe_route_backward(int64_t n, int64_t topk, int64_t experts, cons
  *   flags     THL_MOE_GATED and at most one of THL_MOE_RELU, THL_MOE_GELU (the
  *             erf form) and THL_MOE_SILU
  *   types     X F16 or BF16; Y F32, F16 or BF16
- * Sums are fp32; u is kept with 16 significant bits (magnitudes above bf16's
- * largest, 3.39e38, count as infinite); Y rounds once.  A token that holds an
+ * Sums and u are fp32; Y rounds once.  A token that holds an
  * infinity or NaN gives infinities or NaN; other tokens do not see it.
  * n * topk <= 1024 (THL_ERR_UNSUPPORTED above): every 8 to 32 choices of an
  * expert stream its weights once more.  experts * stride (of each stride) at

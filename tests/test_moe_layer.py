@@ -361,3 +361,59 @@ def test_torch_form_refusals(bad):
         else:
             thl.moe_layer(xt[:1].expand(1025, 64), ids[:1, :1].expand(1025, 1), torch.ones(1025, 1, device=DEV), w1, w2,
                           torch.empty(1025, 64, device=DEV), **call)
+
+
+def _unit(w, k):
+    """The matrix that passes k values on, as stored, with its scales."""
+    one = torch.eye(k)
+    if w == "e2m1":
+        codes = (2 * one).to(torch.uint8)  # code 2 is 1
+        return (codes[:, 0::2] | (codes[:, 1::2] << 4))[None].to(DEV), torch.full((1, k, -(-k // 32)), 127, dtype=torch.uint8, device=DEV)
+    if w == "e4m3":
+        return one.to(F["e4m3"])[None].to(DEV), torch.full((1, k, -(-k // 32)), 127, dtype=torch.uint8, device=DEV)
+    return one.to(F[w])[None].to(DEV), None
+
+
+@pytest.mark.parametrize("w", KINDS)
+@pytest.mark.parametrize("k", [34, 64, 300, 520])
+@pytest.mark.parametrize("n", [1, 3, 4, 5, 9, 17, 40])
+def test_u_has_the_bits_of_fp32(w, k, n):
+    """u = gate * up of two numbers of 17 bits, rounded to fp32 once, passed on by the second matrix: bit for bit."""
+    g = torch.Generator().manual_seed(k + n)
+    x = torch.zeros(n, k)
+    x[:, :4] = torch.tensor([1.0, 2.0 ** -4, 2.0 ** -8, 2.0 ** -12]) * (1.0 - 2.0 * torch.randint(0, 2, (n, 4), generator=g))
+    w2, sf2 = _unit(w, k)
+    if w == "e2m1":
+        w1 = torch.randint(0, 256, (1, 2 * k, k // 2), generator=g).to(torch.uint8)
+        v1 = ref.e2m1_values(w1[0], k)
+    else:
+        v1 = torch.randint(-15, 16, (2 * k, k), generator=g).double() / 8
+        w1 = v1.float()[None].to(F[w])
+    sf1 = None if sf2 is None else torch.full((1, 2 * k, sf2.shape[2]), 127, dtype=torch.uint8, device=DEV)
+    y = torch.full((n, k), float("nan"), device=DEV)
+    thl.moe_layer(x.to(F["f16" if w == "f16" else "bf16"]).to(DEV), torch.zeros(n, 1, dtype=torch.int32, device=DEV),
+                  torch.ones(n, 1, device=DEV), w1.to(DEV), w2, y, act="none", sf1=sf1, sf2=sf2)
+    torch.cuda.synchronize()
+    pre = x.double() @ v1.t()
+    assert bool((pre.float().double() == pre).all())  # multiples of 2^-15 below 8
+    want = pre[:, :k].float() * pre[:, k:].float()
+    assert torch.equal(y.cpu(), want), float(((y.cpu() - want).abs() / want.abs().clamp(min=1e-30)).max())
+
+
+def test_u_of_the_whole_range_of_fp32():
+    # between bf16's largest number and fp32's
+    n, k = 3, 64
+    x = torch.zeros(n, k, dtype=torch.bfloat16, device=DEV)
+    x[:, 0], x[:, 1] = 2.0 ** 64, 2.0 ** 50
+    x[1] = -x[1]
+    w1 = torch.zeros(1, k, k, dtype=torch.bfloat16, device=DEV)
+    w1[:, :, 0] = torch.finfo(torch.bfloat16).max / 2.0 ** 64
+    w1[:, :, 1] = 1.5 * 2.0 ** (119 - 50)  # three quarters of a step of bf16
+    w2, _ = _unit("bf16", k)
+    y = torch.empty(n, k, device=DEV)
+    thl.moe_layer(x, torch.zeros(n, 1, dtype=torch.int32, device=DEV), torch.ones(n, 1, device=DEV), w1, w2, y, gated=False,
+                  act="none")
+    torch.cuda.synchronize()
+    want = (ref.f64(x) @ ref.f64(w1[0]).t()).float()
+    assert bool(torch.isfinite(want).all()) and float(want.max()) > torch.finfo(torch.bfloat16).max * (1 + 2.0 ** -9)
+    assert torch.equal(y.cpu(), want)

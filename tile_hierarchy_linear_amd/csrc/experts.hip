@@ -15,10 +15,9 @@
 //
 // Products are exact and their sums fp32.  The first multiplies activations of
 // bf16 or fp16 with weights of their type, or MX weights decoded to it.  u is
-// computed in fp32 and taken as a sum of two bf16 numbers, its value rounded to
-// eight bits and the rest, which leaves 2^-17 of the value; the second product
-// adds those of both, and fp16 weights are, exactly, two bf16 numbers as well.
-// (fp16 for u would do for its bits but not for its range.)
+// computed in fp32 and taken as the sum of three bf16 numbers, eight of its bits
+// each; the second product adds those of all three, and fp16 weights are,
+// exactly, two bf16 numbers as well.
 //
 // Measured, silu, gated, bf16 activations: one token of 4096 features, 8 of 128
 // experts of 1024 E2M1, 20.9 us (13 and 9; its 53 MB at what HBM copies are 9,
@@ -37,7 +36,7 @@ namespace thl {
 namespace {
 
 enum : int { W_B16 = 0, W_H16 = 1, W_E4M3 = 2, W_E2M1 = 3 };
-enum : int { X_B16 = 0, X_H16 = 1, X_PAIR = 2 };  // PAIR: u as two planes
+enum : int { X_B16 = 0, X_H16 = 1, X_PLANES = 2 };  // PLANES: u as three bf16 numbers
 
 constexpr int64_t kMaxPairs = 1024;  // choices of all tokens
 constexpr int kWaves = 4;
@@ -50,6 +49,9 @@ constexpr int kWaves = 4;
 // 69.6 with two; E4M3 50.2 and 117.6, 53.1 and 97.0.  bf16 with 128 experts,
 // 3 choices each: 112.9 with one, 103.9 with two.
 constexpr int most_tiles(int wk) { return wk == W_E2M1 ? 1 : 2; }
+
+// Choices of a pass over an expert's weights in the second product.
+constexpr int choices_of_pass(bool many) { return many ? 16 : 4; }
 
 // Values of K in 16 bytes of a row.
 constexpr int piece_of(int wk) { return wk == W_E2M1 ? 32 : (wk == W_E4M3 ? 16 : 8); }
@@ -64,21 +66,20 @@ struct ExpertArgs {
   const uint8_t* w;
   const uint8_t* sf;
   const void* bias;
-  const uint16_t* x;   // X, or u's first plane
-  const uint16_t* lo;  // u's second plane
+  const uint16_t* x;  // X, or u's first plane
   const void* ids;
   const float* weights;
   void* y;
   // the workspace: u's planes, z of every choice, each slot, and the choices by
   // expert
-  uint16_t* u_hi;
-  uint16_t* u_lo;
+  uint16_t* u;
   float* z;
   Slot* slots;
   int32_t* order;
   int64_t w_row, w_expert;  // bytes
   int64_t ld_sf, sf_expert, bias_expert;
   int64_t ldx, ldy, ld_u, ld_ids;
+  int64_t plane;            // values from one of u's to the next
   int64_t row_bytes;        // of K weights
   int32_t k, features;      // of an output: hidden features, or the layer's
   int32_t pairs, topk, experts, ids_bytes;
@@ -116,12 +117,20 @@ __device__ __forceinline__ void split_h(v4i x, v4i& hi, v4i& lo) {
     lo[d] = static_cast<int>(__builtin_amdgcn_perm(l[1], l[0], 0x07060302u));
   }
 }
-// u as two planes.
-__device__ __forceinline__ void split_f(float v, uint16_t& hi, uint16_t& lo) {
-  const __bf16 h = static_cast<__bf16>(v);
-  const float f = static_cast<float>(h);
-  hi = __builtin_bit_cast(uint16_t, h);
-  lo = __builtin_fabsf(f) < INFINITY ? __builtin_bit_cast(uint16_t, static_cast<__bf16>(v - f)) : 0;
+// u as three planes: its first eight bits, the next eight and the last, exact
+// but for what lies below 2^-133, the smallest bf16 number.  Infinities and NaN
+// have no rest.
+__device__ __forceinline__ void split_f(float v, uint16_t (&o)[3]) {
+#pragma clang fp contract(off)  // (of v's value as rounded, not of the product that gave it)
+  const bool rest = __builtin_fabsf(v) < INFINITY;
+  const uint16_t quiet = v != v ? 0x0040 : 0;  // a NaN stays one
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    const uint32_t top = __builtin_bit_cast(uint32_t, v) & 0xffff0000u;
+    o[p] = static_cast<uint16_t>(top >> 16);
+    v = rest ? v - __builtin_bit_cast(float, top) : 0.0f;
+  }
+  o[0] |= quiet;
 }
 
 // Codes 8 s .. 8 s + 7 of a piece, times `scale`, a power of two: as fp16 if H,
@@ -188,15 +197,17 @@ __device__ __forceinline__ float activated(float v, int act) {
 // order within a lane, so step s of half h multiplies values
 // chunk + PK (4 h + g) + 8 s .. + 7 of choices and features alike.
 //
-// A tile's sixteen rows are sixteen choices, or of u both planes of eight: rows
-// 8 .. 15 then are the second planes of choices 0 .. 7, and their sums are added
-// at the end.  (Planes as products of their own would need twice the operands.)
+// A tile's sixteen rows are sixteen choices, and of u there are three such tiles,
+// one of each plane.  Of up to four choices one tile holds all planes: rows
+// 4 p .. 4 p + 3 are plane p of choices 0 .. 3 (the last four rows repeat plane 2 and
+// are not used), so that lane group p ends with the sums of plane p, which are
+// added at the end.  (Two such tiles for five to eight choices gave and took:
+// 48 tokens, 8 of 64 experts of 4096 x 1024 bf16, 301 us for 305; 64 tokens, 4 of 32
+// experts of 2048 x 1024, 113.5 for 111.6.)
 template <int WK, int XK>
 struct Kind {
   static constexpr bool MX = WK == W_E4M3 || WK == W_E2M1;
   static constexpr bool HALF = XK == X_H16;  // fp16 by fp16; else bf16 by bf16
-  static constexpr bool PLANES = XK == X_PAIR;
-  static constexpr int CAP = PLANES ? 8 : 16;  // choices of a tile
   static constexpr int PK = piece_of(WK), KC = 8 * PK, STEPS = PK / 8;
 };
 
@@ -280,11 +291,13 @@ struct Stream {
 
 // The sums over a wavefront's started stream and, if it is its, K's partial
 // chunk, of RT tiles of features (w, sf: this lane's rows) and MT tiles of
-// choices (x: this lane's rows).
-template <int WK, int XK, int RT, int MT, int D>
+// choices (x: this lane's rows), each with its sums; or the last with its own and
+// the others with one.
+template <int WK, int XK, int RT, int MT, int AT, int D>
 __device__ __forceinline__ void products(const ExpertArgs& a, const uint8_t* const (&w)[RT],
                                          const uint8_t* const (&sf)[RT], const uint16_t* const (&x)[MT],
-                                         Stream<WK, RT, D>& st, v4f (&acc)[RT][MT]) {
+                                         Stream<WK, RT, D>& st, v4f (&acc)[RT][AT]) {
+  constexpr auto sum_of = [](int t) { return AT == MT ? t : (t == MT - 1 ? AT - 1 : 0); };
   using T = Kind<WK, XK>;
   constexpr int PK = T::PK, KC = T::KC, STEPS = T::STEPS;
   using S = Scales<WK, T::HALF>;
@@ -305,12 +318,15 @@ __device__ __forceinline__ void products(const ExpertArgs& a, const uint8_t* con
           v4i hi, lo;
           split_h(wh[r], hi, lo);
 #pragma unroll
-          for (int t = 0; t < MT; ++t) acc[r][t] = mfma_bf(xh[t][s], lo, mfma_bf(xh[t][s], hi, acc[r][t]));
+          for (int t = 0; t < MT; ++t) {
+            v4f& sum = acc[r][sum_of(t)];
+            sum = mfma_bf(xh[t][s], lo, mfma_bf(xh[t][s], hi, sum));
+          }
         } else {
           v4i q = wh[r];
           if constexpr (T::MX) q = decode<WK, T::HALF>(q, s, S::decoding(code[r]));
 #pragma unroll
-          for (int t = 0; t < MT; ++t) acc[r][t] = multiply(xh[t][s], q, acc[r][t]);
+          for (int t = 0; t < MT; ++t) acc[r][sum_of(t)] = multiply(xh[t][s], q, acc[r][sum_of(t)]);
         }
       }
   };
@@ -333,7 +349,7 @@ __device__ __forceinline__ void products(const ExpertArgs& a, const uint8_t* con
             alone = multiply(u, v, alone);
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[r][t][e] += factor * alone[e];
+          for (int e = 0; e < 4; ++e) acc[r][sum_of(t)][e] += factor * alone[e];
         }
       }
     }
@@ -397,7 +413,7 @@ __device__ __forceinline__ void products(const ExpertArgs& a, const uint8_t* con
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int t = 0; t < MT; ++t) acc[r][t] *= exp2_of(127 - S::SHIFT);
+      for (int t = 0; t < AT; ++t) acc[r][t] *= exp2_of(127 - S::SHIFT);
   }
 
   // The halves that were skipped, and K's partial chunk (whose number is
@@ -466,7 +482,6 @@ __device__ __forceinline__ void row_of(const ExpertArgs& a, int64_t expert, int 
 // their gates multiply); its wavefronts split K.
 template <int WK, int XK, bool GATED>
 __global__ void __launch_bounds__(64 * kWaves, 2) experts_up_kernel(ExpertArgs a) {
-  using T = Kind<WK, XK>;
   constexpr int RT = GATED ? 2 : 1, MOST = most_tiles(WK), D = 2;
   __shared__ int list[kMaxPairs];
   __shared__ int hits[2][kWaves];
@@ -529,11 +544,11 @@ __global__ void __launch_bounds__(64 * kWaves, 2) experts_up_kernel(ExpertArgs a
     const uint16_t* x[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const int i = first + T::CAP * t + col;
+      const int i = first + 16 * t + col;
       x[t] = a.x + static_cast<int64_t>(list[i < count ? i : count - 1] / a.topk) * a.ldx;
     }
     v4f acc[RT][MT] = {};
-    products<WK, XK, RT, MT, D>(a, w, sf, x, st, acc);
+    products<WK, XK, RT, MT, MT, D>(a, w, sf, x, st, acc);
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -542,7 +557,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) experts_up_kernel(ExpertArgs a
         for (int e = 0; e < 4; ++e) part[wave][r][t][e][lane] = acc[r][t][e];
   };
   for (int first = 0; first < count;) {
-    const int left = count - first, tiles = left > T::CAP ? MOST : 1;
+    const int left = count - first, tiles = left > 16 ? MOST : 1;
     __syncthreads();  // the sums before these have been read
     if (MOST == 1 || tiles == 1)
       run(first, std::integral_constant<int, 1>{});
@@ -552,7 +567,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) experts_up_kernel(ExpertArgs a
     // Register e of lane l is choice 4 (l / 16) + e of the tile and feature l % 16.
     static_assert(kWaves == 4, "a wavefront finishes one register");
     for (int t = 0; t < tiles; ++t) {
-      const int i = T::CAP * t + 4 * g + wave;
+      const int i = 16 * t + 4 * g + wave;
       if (i >= left) continue;
       auto sum = [&](int r) {
         float v = 0.0f;
@@ -572,12 +587,12 @@ __global__ void __launch_bounds__(64 * kWaves, 2) experts_up_kernel(ExpertArgs a
         if (a.bias) m += load_f(a.bias, a.bias_type, b + a.features);
         v *= m;
       }
-      uint16_t hi, lo;
-      split_f(v, hi, lo);
-      a.u_hi[at * a.ld_u + f] = hi;
-      a.u_lo[at * a.ld_u + f] = lo;
+      uint16_t u[3];
+      split_f(v, u);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) a.u[p * a.plane + at * a.ld_u + f] = u[p];
     }
-    first += T::CAP * tiles;
+    first += 16 * tiles;
     if (first < count) st.start(a, w, sf);
   }
 }
@@ -585,43 +600,47 @@ __global__ void __launch_bounds__(64 * kWaves, 2) experts_up_kernel(ExpertArgs a
 // ---- the second product
 // The sums of an expert's choices over a wavefront's started stream, handed to
 // `put(place in `order`, choice, tile, feature of it, value)` by the lanes that hold
-// them, planes added.  At most MOST tiles of choices at a time.
-template <int WK, int RT, int MOST, int D, class Put>
+// them, planes added.  MANY: up to sixteen choices a pass, else up to four.
+template <int WK, bool MANY, int RT, int D, class Put>
 __device__ __forceinline__ void down_choices(const ExpertArgs& a, const uint8_t* const (&w)[RT],
                                              const uint8_t* const (&sf)[RT], Stream<WK, RT, D>& st, const int* order,
                                              int count, Put put) {
-  using T = Kind<WK, X_PAIR>;
   const int lane = static_cast<int>(threadIdx.x) & 63, col = lane & 15, g = lane >> 4;
-  auto run = [&](int first, auto tiles) {
-    constexpr int MT = decltype(tiles)::value;
-    const uint16_t* x[MT];
+  auto row = [&](int i, int p) {  // of u, of a choice that exists
+    return a.x + p * a.plane + static_cast<int64_t>(order[i < count ? i : count - 1]) * a.ldx;
+  };
+  for (int first = 0; first < count; first += choices_of_pass(MANY)) {
+    if (first > 0) st.start(a, w, sf);
+    if (!MANY || count - first <= 4) {
+      const uint16_t* x[1] = {row(first + (col & 3), col < 12 ? col >> 2 : 2)};
+      v4f acc[RT][1] = {};
+      products<WK, X_PLANES, RT, 1, 1, D>(a, w, sf, x, st, acc);
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const int i = first + T::CAP * t + (col & 7);
-      x[t] = (col >= 8 ? a.lo : a.x) + static_cast<int64_t>(order[i < count ? i : count - 1]) * a.ldx;
-    }
-    v4f acc[RT][MT] = {};
-    products<WK, X_PAIR, RT, MT, D>(a, w, sf, x, st, acc);
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
+      for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float v = acc[r][t][e] + __shfl_xor(acc[r][t][e], 32);
-          const int i = first + T::CAP * t + 4 * g + e;
-          if (g < 2 && i < count) put(i, order[i], r, col, v);
+          const float v = acc[r][0][e], rest = __shfl_xor(v, 16) + __shfl_xor(v, 32);
+          const int i = first + e;
+          if (g == 0 && i < count) put(i, order[i], r, col, v + rest);
         }
-  };
-  for (int first = 0; first < count;) {
-    if (MOST == 1 || count - first <= T::CAP) {
-      run(first, std::integral_constant<int, 1>{});
-      first += T::CAP;
-    } else {
-      run(first, std::integral_constant<int, MOST>{});
-      first += MOST * T::CAP;
+    } else if constexpr (MANY) {
+      const uint16_t* x[3];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) x[p] = row(first + col, 2 - p);
+      // of planes 1 and 2, and of plane 0 (of MX weights all in one: the registers of
+      // two cost E4M3 a third of its wavefronts, 32 tokens, 8 of 128 experts of 2048 x
+      // 768, 137 us for 129)
+      constexpr int AT = Kind<WK, X_PLANES>::MX ? 1 : 2;
+      v4f acc[RT][AT] = {};
+      products<WK, X_PLANES, RT, 3, AT, D>(a, w, sf, x, st, acc);
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = first + 4 * g + e;
+          if (i < count) put(i, order[i], r, col, AT == 1 ? acc[r][0][e] : acc[r][AT - 1][e] + acc[r][0][e]);
+        }
     }
-    if (first < count) st.start(a, w, sf);
   }
 }
 
@@ -639,7 +658,7 @@ __device__ __forceinline__ void store_y(const ExpertArgs& a, int64_t j, int64_t 
 // the slots (`ks` of them share one slot's K), and adds each token's choices.
 constexpr int kJoinWaves = 8, kJoinPairs = 64;
 
-template <int WK>
+template <int WK, bool MANY>
 __global__ void __launch_bounds__(64 * kJoinWaves, 2) experts_down_join_kernel(ExpertArgs a, int ks) {
   constexpr int D = 2;
   extern __shared__ int shared[];
@@ -670,8 +689,8 @@ __global__ void __launch_bounds__(64 * kJoinWaves, 2) experts_down_join_kernel(E
       copied = true;
     }
     if (s.count > 0)
-      down_choices<WK, 1, most_tiles(WK), D>(a, w, sf, st, order + s.start, s.count,
-                             [&](int, int p, int, int f, float v) { mine[p * 16 + f] = v; });
+      down_choices<WK, MANY, 1, D>(a, w, sf, st, order + s.start, s.count,
+                                   [&](int, int p, int, int f, float v) { mine[p * 16 + f] = v; });
   }
   __syncthreads();
   const int n = a.pairs / a.topk;
@@ -694,10 +713,9 @@ __global__ void __launch_bounds__(64 * kJoinWaves, 2) experts_down_join_kernel(E
 // More of them: a workgroup takes RT tiles of features of one slot, its
 // wavefronts splitting K; z goes to the workspace, and a third launch adds
 // each token's choices.
-template <int WK>
+template <int WK, bool MANY>
 __global__ void __launch_bounds__(64 * kWaves, 2) experts_down_kernel(ExpertArgs a) {
-  using T = Kind<WK, X_PAIR>;
-  constexpr int RT = 2, D = 2, MOST = most_tiles(WK), ROWS = MOST * T::CAP;
+  constexpr int RT = 2, D = 2, ROWS = choices_of_pass(MANY);
   __shared__ float part[kWaves][ROWS][16 * RT];
   const int tid = static_cast<int>(threadIdx.x), col = tid & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -715,7 +733,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) experts_down_kernel(ExpertArgs
     st.start(a, w, sf);
     const int left = count - first < ROWS ? count - first : ROWS;
     __syncthreads();  // the sums before these have been read
-    down_choices<WK, RT, MOST, D>(a, w, sf, st, order + first, left,
+    down_choices<WK, MANY, RT, D>(a, w, sf, st, order + first, left,
                                   [&](int i, int, int r, int f, float v) { part[wave][i][16 * r + f] = v; });
     __syncthreads();
     for (int q = tid; q < left * 16 * RT; q += 64 * kWaves) {
@@ -783,7 +801,7 @@ hipError_t launch_up(ExpertArgs& a, thl_dtype w, bool x_bf, bool gated, hipStrea
   }
 }
 
-template <int WK>
+template <int WK, bool MANY>
 hipError_t launch_down(ExpertArgs& a, hipStream_t st) {
   const int64_t tiles = (static_cast<int64_t>(a.features) + 15) / 16;
   // Products and joining in one launch save a launch of 4.7 us, but every
@@ -799,12 +817,12 @@ hipError_t launch_down(ExpertArgs& a, hipStream_t st) {
     int ks = 1;
     while (2 * ks * a.slot_count <= kJoinWaves) ks *= 2;
     void* args[] = {&a, &ks};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&experts_down_join_kernel<WK>),
+    return hipLaunchKernel(reinterpret_cast<const void*>(&experts_down_join_kernel<WK, MANY>),
                            dim3(static_cast<unsigned>(tiles)), dim3(64 * kJoinWaves), args,
                            static_cast<unsigned>(4 * a.pairs * (3 + 16 * ks)), st);
   }
   void* args[] = {&a};
-  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(&experts_down_kernel<WK>),
+  const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(&experts_down_kernel<WK, MANY>),
                                        dim3(static_cast<unsigned>((tiles + 1) / 2), static_cast<unsigned>(a.slot_count)),
                                        dim3(64 * kWaves), args, 0, st);
   if (e != hipSuccess) return e;
@@ -815,13 +833,18 @@ hipError_t launch_down(ExpertArgs& a, hipStream_t st) {
 hipError_t launch_down(ExpertArgs& a, thl_dtype w, hipStream_t st) {
   switch (w) {
     case THL_BF16:
-      return launch_down<W_B16>(a, st);
+      return launch_down<W_B16, true>(a, st);
     case THL_F16:
-      return launch_down<W_H16>(a, st);
+      return launch_down<W_H16, true>(a, st);
     case THL_E4M3:
-      return launch_down<W_E4M3>(a, st);
+      return launch_down<W_E4M3, true>(a, st);
     default:
-      return launch_down<W_E2M1>(a, st);
+      // Sixteen choices a pass of E2M1 weights take 228 registers (146 with four) and
+      // so a third of the wavefronts: at two choices a slot or fewer the passes are
+      // four.  The layer of 2048 x 768, 8 of 128 experts, four a pass and sixteen: 4
+      // tokens 33.9 and 36.7 us, 16 66.3 and 69.6, 32 (two a slot) 91.7 and 93.0, 48
+      // 116 and 113, 96 179 and 164.
+      return a.pairs > 2 * a.slot_count ? launch_down<W_E2M1, true>(a, st) : launch_down<W_E2M1, false>(a, st);
   }
 }
 
@@ -873,7 +896,7 @@ extern "C" {
 size_t thl_moe_layer_workspace(int64_t m, int64_t hidden, int64_t n, int64_t topk) {
   if (m <= 0 || m > kMaxFeatures || hidden <= 0 || hidden > kMaxFeatures || n <= 0 || topk <= 0) return 0;
   if (n > kMaxPairs || topk > kMaxPairs || n * topk > kMaxPairs) return 0;
-  return static_cast<size_t>(n * topk) * 4 * static_cast<size_t>(pitch(hidden) + m + 3);
+  return static_cast<size_t>(n * topk) * static_cast<size_t>(6 * pitch(hidden) + 4 * (m + 3));
 }
 
 thl_status thl_moe_layer(int64_t m, int64_t hidden, int64_t n, int64_t topk, int64_t experts, const void* X,
@@ -927,8 +950,8 @@ thl_status thl_moe_layer(int64_t m, int64_t hidden, int64_t n, int64_t topk, int
   a.by_choice = pairs < experts;
   a.slot_count = a.by_choice ? a.pairs : a.experts;
   a.weights = weights, a.y = Y, a.ldy = ldy, a.y_type = type_y;
-  a.u_hi = static_cast<uint16_t*>(workspace), a.u_lo = a.u_hi + pairs * ld_u, a.ld_u = ld_u;
-  a.z = reinterpret_cast<float*>(a.u_lo + pairs * ld_u);
+  a.u = static_cast<uint16_t*>(workspace), a.ld_u = ld_u, a.plane = pairs * ld_u;
+  a.z = reinterpret_cast<float*>(a.u + 3 * a.plane);
   a.slots = reinterpret_cast<Slot*>(a.z + pairs * m), a.order = reinterpret_cast<int32_t*>(a.slots + pairs);
 
   matrix(a, *up, m);
@@ -937,7 +960,7 @@ thl_status thl_moe_layer(int64_t m, int64_t hidden, int64_t n, int64_t topk, int
   hipError_t e = launch_up(a, up->type, type_x == THL_BF16, gated, stream);
   if (e == hipSuccess) {
     matrix(a, *down, hidden);
-    a.x = a.u_hi, a.lo = a.u_lo, a.ldx = ld_u, a.features = static_cast<int32_t>(m);
+    a.x = a.u, a.ldx = ld_u, a.features = static_cast<int32_t>(m);
     e = launch_down(a, down->type, stream);
   }
   return e == hipSuccess ? THL_OK : THL_ERR_HIP;
