@@ -417,3 +417,31 @@ def test_u_of_the_whole_range_of_fp32():
     want = (ref.f64(x) @ ref.f64(w1[0]).t()).float()
     assert bool(torch.isfinite(want).all()) and float(want.max()) > torch.finfo(torch.bfloat16).max * (1 + 2.0 ** -9)
     assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("w", KINDS)
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_nan_goes_through_every_activation(w, act, gated):
+    xt, ids, wt, w1, w2, yt, call = _layer(5, 160, 64, 2, 1, w=w, ids=torch.ones(5, 1), act=act, gated=gated, exact=False)
+    x, y = xt.clone(), torch.empty_like(yt)
+    x[3, 159] = float("nan")
+    thl.moe_layer(x, ids, wt, w1, w2, y, **call)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(y[3]).all()) and torch.equal(y[[0, 1, 2, 4]], yt[[0, 1, 2, 4]])
+    # one row of the first matrix: every token of the expert
+    bad, call = w1.clone(), dict(call)
+    if w in ("e4m3", "e2m1"):
+        call["sf1"] = call["sf1"].clone()
+        call["sf1"][1, 5, 2] = 255
+    else:
+        bad[1, 5, 70] = float("nan")
+    thl.moe_layer(xt, ids, wt, bad, w2, y, **call)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(y).all())
+    ids = torch.tensor([[1], [0], [1], [0], [-1]], dtype=torch.int32, device=DEV)
+    thl.moe_layer(xt, ids, wt, w1, w2, yt, **call)  # (call: the scales with the NaN, the weights without)
+    thl.moe_layer(xt, ids, wt, bad, w2, y, **call)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(y[[0, 2]]).all()) and bool(torch.isfinite(y[[1, 3, 4]]).all())
+    assert torch.equal(y[[1, 3, 4]], yt[[1, 3, 4]])

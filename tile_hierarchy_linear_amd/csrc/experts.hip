@@ -186,7 +186,7 @@ struct Scales {
 };
 
 __device__ __forceinline__ float activated(float v, int act) {
-  if (act & THL_MOE_RELU) return v > 0.0f ? v : 0.0f;
+  if (act & THL_MOE_RELU) return v <= 0.0f ? 0.0f : v;  // (NaN stays)
   if (act & THL_MOE_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752440f));
   if (act & THL_MOE_SILU) return v / (1.0f + expf(-v));
   return v;
