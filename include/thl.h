@@ -635,9 +635,9 @@ thl_status thl_moe_route_backward(int64_t n, int64_t topk, int64_t experts, cons
  *             erf form) and THL_MOE_SILU
  *   types     X F16 or BF16; Y F32, F16 or BF16
  * Sums and u are fp32; Y rounds once.  A NaN in a token, a matrix's row or a
- * block's scale goes through every activation to all that is computed from it, an
- * infinity as the formulas have it (of -infinity the RELU is 0, the other two NaN);
- * other tokens and experts do not see it.
+ * block's scale goes through every activation to all that is computed from it; an
+ * infinity gives infinities or NaN wherever the formulas do (of -infinity the RELU
+ * is 0, the other two are NaN).  Other tokens and experts do not see it.
  * n * topk <= 1024 (THL_ERR_UNSUPPORTED above): every 4 to 32 choices of an
  * expert stream its weights once more.  experts * stride (of each stride) at
  * most 2^40 (THL_ERR_UNSUPPORTED above).

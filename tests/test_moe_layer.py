@@ -445,3 +445,22 @@ def test_nan_goes_through_every_activation(w, act, gated):
     torch.cuda.synchronize()
     assert bool(torch.isnan(y[[0, 2]]).all()) and bool(torch.isfinite(y[[1, 3, 4]]).all())
     assert torch.equal(y[[1, 3, 4]], yt[[1, 3, 4]])
+
+
+@pytest.mark.parametrize("w", ["bf16", "f16"])
+@pytest.mark.parametrize("n,experts", [(1, 3), (4, 1), (9, 2), (40, 2)])
+def test_an_infinite_weight_of_the_second_matrix(w, n, experts):
+    xt, ids, wt, w1, w2, yt, call = _layer(n, 70, 40, experts, 1, w=w, gated=False, ids=torch.zeros(n, 1))
+    u = ref.f64(xt) @ ref.f64(w1[0]).t()
+    c = int(u.abs().amin(dim=0).argmax())
+    bad, y = w2.clone(), torch.empty_like(yt)
+    bad[0, 3, c], bad[0, 69, c] = float("inf"), -float("inf")
+    thl.moe_layer(xt, ids, wt, w1, bad, y, **call)
+    torch.cuda.synchronize()
+    assert bool(u[:, c].ne(0).any())
+    for row, sign in ((3, 1), (69, -1)):
+        want = torch.where(u[:, c] == 0, torch.nan, sign * torch.copysign(torch.full((), torch.inf).double(), u[:, c]))
+        assert torch.equal(y[:, row].cpu().double().nan_to_num(nan=7.0, posinf=1.0, neginf=-1.0),
+                           want.nan_to_num(nan=7.0, posinf=1.0, neginf=-1.0))
+    rest = [i for i in range(70) if i not in (3, 69)]
+    assert torch.equal(y[:, rest], yt[:, rest])

@@ -133,6 +133,12 @@ __device__ __forceinline__ void split_f(float v, uint16_t (&o)[3]) {
   o[0] |= quiet;
 }
 
+// Sums of plane 0 and of the others.  An infinite weight makes the first infinite
+// and, of planes of zeros, the others NaN.
+__device__ __forceinline__ float planes_sum(float first, float rest) {
+  return __builtin_fabsf(first) < INFINITY ? first + rest : first;
+}
+
 // Codes 8 s .. 8 s + 7 of a piece, times `scale`, a power of two: as fp16 if H,
 // else as bf16.
 template <int WK, bool H>
@@ -621,7 +627,7 @@ __device__ __forceinline__ void down_choices(const ExpertArgs& a, const uint8_t*
         for (int e = 0; e < 4; ++e) {
           const float v = acc[r][0][e], rest = __shfl_xor(v, 16) + __shfl_xor(v, 32);
           const int i = first + e;
-          if (g == 0 && i < count) put(i, order[i], r, col, v + rest);
+          if (g == 0 && i < count) put(i, order[i], r, col, planes_sum(v, rest));
         }
     } else if constexpr (MANY) {
       const uint16_t* x[3];
@@ -638,7 +644,7 @@ __device__ __forceinline__ void down_choices(const ExpertArgs& a, const uint8_t*
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = first + 4 * g + e;
-          if (i < count) put(i, order[i], r, col, AT == 1 ? acc[r][0][e] : acc[r][AT - 1][e] + acc[r][0][e]);
+          if (i < count) put(i, order[i], r, col, AT == 1 ? acc[r][0][e] : planes_sum(acc[r][AT - 1][e], acc[r][0][e]));
         }
     }
   }
