@@ -349,3 +349,28 @@ def test_longest_tokens():
     assert bool(((dx.double() - want).abs() <= bound + ref.half_step(want, dx.dtype) * 1.01).all())
     assert bool(((dw.double() - (G * h)[0]).abs() <= 2 * G[0].abs() * e_h[0] + 4 * ref.U * (G * h)[0].abs()).all())
     assert torch.equal(db, dy[0].float())
+
+
+@pytest.mark.parametrize("kind", ["e2m1", "e4m3", "e5m2"])
+@pytest.mark.parametrize("m", [33, 300, 2050, 5000, 16400])
+@pytest.mark.parametrize("eps", [EPS, 0.0])
+def test_nan_in_mx_blocks(kind, m, eps):
+    """The blocks of the norm are thl.mx_quantize's of its fp32 output: scale 255 (NaN) where one holds a NaN."""
+    x = _rand(m, 6, m, dtype="bf16", shift=0.5)
+    x[1, 7], x[2, m - 1], x[4] = float("inf"), float("nan"), 3.0  # (equal features: 0 / 0 with eps = 0)
+    w, b = 1 + 0.2 * _rand(1, m), _rand(2, m)
+    w[m // 2], b[m - 1] = float("inf"), float("nan")
+    full = torch.empty(6, m, device="cuda")
+    thl.layernorm(x, w, b, full, eps=eps)
+    got, want = ([torch.full((6, (m + 1) // 2 if kind == "e2m1" else m), 0xEE, dtype=torch.uint8, device="cuda"),
+                  torch.full((6, (m + 31) // 32), 0xEE, dtype=torch.uint8, device="cuda")] for _ in range(2))
+    typed = [v if kind == "e2m1" else v.view(F[kind]) for v in (got[0], want[0])]
+    thl.layernorm(x, w, b, typed[0], eps=eps, sf=got[1])
+    thl.mx_quantize(full, typed[1], want[1])
+    torch.cuda.synchronize()
+    assert torch.equal(got[1], want[1]) and torch.equal(got[0], want[0])
+    gone = [1, 2] + ([4] if eps == 0.0 else [])
+    assert bool((got[1][gone] == 255).all()) and bool((got[0][gone] == 0).all())
+    assert bool((got[1][:, -1] == 255).all())  # the bias's NaN
+    last = torch.tensor([0, 3, 5])
+    assert bool((got[1][last, :(m - 1) // 32] < 255).all()) and bool((got[0][last, :16] != 0).any())

@@ -33,7 +33,9 @@ struct NormArgs {
 
 // Features e .. e+7 of a token's output (those past m take part in the
 // block maximum as zeros and are not stored).  Called by whole groups of
-// four consecutive lanes, which hold one MX block.
+// four consecutive lanes, which hold one MX block.  Centred: a block with a NaN
+// has the scale NaN and elements of zero.
+template <bool CENTRED>
 __device__ __forceinline__ void store_out(const NormArgs& a, int64_t row, int e, const float (&v)[8]) {
   const int valid = a.m - e;
   if (a.y_mode == Y_FLOAT) {
@@ -53,18 +55,24 @@ __device__ __forceinline__ void store_out(const NormArgs& a, int64_t row, int e,
     return;
   }
   float amax = 0.0f;
+  bool nan = false;  // (which the maximum leaves out)
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < valid) amax = __builtin_fmaxf(amax, __builtin_fabsf(v[i]));
+  for (int i = 0; i < 8; ++i) {
+    if (i < valid) {
+      amax = __builtin_fmaxf(amax, __builtin_fabsf(v[i]));
+      if constexpr (CENTRED) nan = nan || v[i] != v[i];
+    }
+  }
   amax = __builtin_fmaxf(amax, __shfl_xor(amax, 1));
   amax = __builtin_fmaxf(amax, __shfl_xor(amax, 2));
+  if constexpr (CENTRED) nan = ((__ballot(nan) >> (threadIdx.x & 60)) & 15) != 0;
   if (valid <= 0) return;
   const int emax = a.y_type == THL_E2M1X2 ? 2 : (a.y_type == THL_E4M3 ? 8 : 15);
-  const int code = mx_scale_code(amax, emax);
+  const int code = nan ? 255 : mx_scale_code(amax, emax);
   const float inv = __builtin_ldexpf(1.0f, 127 - code);
   float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = v[i] * inv;
+  for (int i = 0; i < 8; ++i) q[i] = nan ? 0.0f : v[i] * inv;
   if (a.y_type == THL_E2M1X2) {
     uint32_t w = 0;
 #pragma unroll
@@ -207,7 +215,7 @@ __global__ void __launch_bounds__(WPR * 64) norm_kernel(NormArgs a) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] = v[c][i] * rho * w[i];
         }
-        store_out(a, row, e, o);
+        store_out<CENTRED>(a, row, e, o);
       }
     }
   } else {
@@ -280,7 +288,7 @@ __global__ void __launch_bounds__(WPR * 64) norm_kernel(NormArgs a) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = v[i] * rho * w[i];
         }
-        store_out(a, row, e, v);
+        store_out<CENTRED>(a, row, e, v);
       }
     }
   }
