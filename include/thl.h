@@ -372,10 +372,12 @@ thl_status thl_gemm_grouped(int64_t count, const thl_group_problem* problems,
  *          BF16.  y: F32, F16 or BF16; E4M3 or E5M2 with sfy = NULL: y *
  *          (1 / y_scale), the reciprocal and the product rounded in fp32 each,
  *          magnitudes past the largest finite value clamped to it (y_scale is
- *          the product's a_scale or b_scale; 1 for every other form); E4M3, E5M2 or E2M1X2 with sfy: MX blocks of 32 consecutive
- *          features by thl_gemm's MX-output rule, SFY(b, j) at
- *          sfy[j*ld_sfy + b], ld_sfy >= ceil(m/32) (a product that reads them
- *          as sfa or sfb wants a multiple of 16), E2M1X2 with ldy even.
+ *          the product's a_scale or b_scale; 1 for every other form); E4M3, E5M2
+ *          or E2M1X2 with sfy: MX blocks of 32 consecutive features by thl_gemm's
+ *          MX-output rule, SFY(b, j) at sfy[j*ld_sfy + b], ld_sfy >= ceil(m/32) (a
+ *          product that reads them as sfa or sfb wants a multiple of 16), E2M1X2
+ *          with ldy even.  A NaN is an element of NaN under the others' scale in
+ *          E4M3 and E5M2; of E2M1X2 its block has scale 255 (NaN) and zeros.
  *   eps    >= 0 and finite.  With eps = 0 a token of zeros is 0/0, NaN.
  * The squares are added in fp32: a token whose sum of them passes fp32's range
  * (features of 1e19, say) gives zeros, and with eps = 0 one whose squares are

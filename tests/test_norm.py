@@ -460,3 +460,23 @@ def test_longest_tokens():
     assert _near(dx, want, bound + ref.half_step(want, dx.dtype) * 1.001)
     want = (G * h)[0]
     assert _near(dw, want, (rel + 4 * ref.U) * want.abs() + ref.half_step(want, dw.dtype))
+
+
+@pytest.mark.parametrize("m", [40, 300, 2050, 16400])
+def test_nan_in_fp4_blocks(m):
+    """A block of E2M1 that holds a NaN has the scale NaN: its elements have no code for one."""
+    x = _rand(m, 4, m, dtype="bf16")
+    x[1, 3] = float("nan")
+    w = torch.ones(m, device="cuda")
+    want = [torch.full((4, (m + 1) // 2), 0xEE, dtype=torch.uint8, device="cuda"), torch.full((4, -(-m // 32)), 0xEE, dtype=torch.uint8, device="cuda")]
+    thl.rmsnorm(x, w, want[0], eps=EPS, sf=want[1])
+    got = [torch.full_like(v, 0xEE) for v in want]
+    w[m - 2] = float("nan")
+    thl.rmsnorm(x, w, got[0], eps=EPS, sf=got[1])
+    torch.cuda.synchronize()
+    assert bool((got[1][1] == 255).all()) and bool((got[0][1] == 0).all())
+    block = (m - 2) // 32
+    assert bool((got[1][:, block] == 255).all()) and bool((got[0][:, 16 * block:16 * block + 16] == 0).all())
+    for j in (0, 2, 3):
+        assert torch.equal(got[1][j, :block], want[1][j, :block])
+        assert torch.equal(got[0][j, :16 * block], want[0][j, :16 * block])

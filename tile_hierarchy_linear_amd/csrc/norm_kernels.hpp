@@ -33,8 +33,9 @@ struct NormArgs {
 
 // Features e .. e+7 of a token's output (those past m take part in the
 // block maximum as zeros and are not stored).  Called by whole groups of
-// four consecutive lanes, which hold one MX block.  Centred: a block with a NaN
-// has the scale NaN and elements of zero.
+// four consecutive lanes, which hold one MX block.  A block with a NaN has the
+// scale NaN and elements of zero; not centred, of 8 bits, elements of NaN under the
+// others' scale.
 template <bool CENTRED>
 __device__ __forceinline__ void store_out(const NormArgs& a, int64_t row, int e, const float (&v)[8]) {
   const int valid = a.m - e;
@@ -60,12 +61,12 @@ __device__ __forceinline__ void store_out(const NormArgs& a, int64_t row, int e,
   for (int i = 0; i < 8; ++i) {
     if (i < valid) {
       amax = __builtin_fmaxf(amax, __builtin_fabsf(v[i]));
-      if constexpr (CENTRED) nan = nan || v[i] != v[i];
+      nan = nan || v[i] != v[i];
     }
   }
   amax = __builtin_fmaxf(amax, __shfl_xor(amax, 1));
   amax = __builtin_fmaxf(amax, __shfl_xor(amax, 2));
-  if constexpr (CENTRED) nan = ((__ballot(nan) >> (threadIdx.x & 60)) & 15) != 0;
+  nan = ((__ballot(nan) >> (threadIdx.x & 60)) & 15) != 0 && (CENTRED || a.y_type == THL_E2M1X2);
   if (valid <= 0) return;
   const int emax = a.y_type == THL_E2M1X2 ? 2 : (a.y_type == THL_E4M3 ? 8 : 15);
   const int code = nan ? 255 : mx_scale_code(amax, emax);
