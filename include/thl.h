@@ -595,7 +595,8 @@ thl_status thl_gemm_w4(int64_t m, int64_t n, int64_t k, const void* W, int64_t l
  *   bias          experts values for the choice alone (may be NULL); one of
  *                 -infinity or NaN keeps its expert from being chosen
  * Computed in fp32.  Without a bias the logits themselves are compared.  A logit
- * of +infinity makes the softmax's weights NaN.  L in F32, F16 or BF16;
+ * of +infinity makes the softmax's weights NaN, and the choice then goes by the
+ * logits with a bias too (one of -infinity or NaN still masks).  L in F32, F16 or BF16;
  * experts <= 1024, topk <= 64 (THL_ERR_UNSUPPORTED above).  No output may
  * overlap another array.
  *

@@ -285,3 +285,33 @@ def test_torch_form_refusals(bad):
             thl.moe_route_backward(l, ids, w, l.half())
         else:
             thl.moe_route(l, ids.cpu(), w)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("experts", [40, 256, 700])
+def test_infinite_logits_and_a_bias(renorm, experts):
+    """Softmax scores of a token with a logit of +infinity are NaN: its weights say so, and the logits alone are compared
+    (a bias still keeps its expert out).  Other tokens and sigmoid scores go on as they are."""
+    l = _rand(experts, 7, experts)
+    plain = l.clone()
+    l[1, 7] = torch.inf
+    l[2, [30, 9]] = torch.inf
+    l[4, 5], l[4, 8:] = torch.inf, -torch.inf
+    bias = _rand(1, 1, experts, scale=0.3)[0].contiguous()
+    bias[9], bias[11] = -torch.inf, float("nan")
+    out = []
+    for v in (plain, l):
+        ids, w = torch.empty(7, 6, dtype=torch.int32, device="cuda"), torch.empty(7, 6, device="cuda")
+        thl.moe_route(v, ids, w, score="softmax", renormalize=renorm, bias=bias)
+        out += [ids.cpu(), w.cpu()]
+    torch.cuda.synchronize()
+    same = [0, 3, 5, 6]
+    assert torch.equal(out[2][same], out[0][same]) and torch.equal(out[3][same], out[1][same])
+    may = torch.isfinite(bias).cpu()
+    for j in (1, 2, 4):
+        by = torch.where(may, l[j].cpu(), -torch.inf)
+        want = [e for e in torch.sort(by, descending=True, stable=True).indices.tolist() if by[e] > -torch.inf][:6]
+        assert out[2][j].tolist() == want + [-1] * (6 - len(want))
+        assert bool(torch.isnan(out[3][j, :len(want)]).all()) and bool((out[3][j, len(want):] == 0).all())
+    ids, w = _run(l, 6, "sigmoid", renorm, bias=torch.where(torch.isfinite(bias), bias, 0.0))
+    assert bool(torch.isfinite(w).all())

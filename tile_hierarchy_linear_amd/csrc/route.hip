@@ -189,17 +189,26 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
     best = wave_max(best);
     const bool soft = a.score == THL_ROUTE_SOFTMAX;
     const float top = best ? value_of(best) : 0.0f;
+    // A logit of +infinity makes every softmax score NaN, which masks no expert: the
+    // logits are compared then, and the weights come out NaN.
+    const bool scores = !soft || top < INFINITY;
     // with the chosen ones' sum alone in the quotient, the others' is not needed
     float x[PER], total = 1.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) x[i] = l[i];
     if (soft && (a.bias || !a.renormalize)) total = softmax_sum<PER>(x, top);
-    if (a.bias) {
+    if (a.bias && scores) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int e = 64 * i + lane;
         const float p = soft ? x[i] / total : sigmoid(l[i]);
         key[i] = key[i] && e < a.experts ? key_of(p + a.bias[e]) : 0u;
+      }
+    } else if (a.bias) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int e = 64 * i + lane;
+        if (e < a.experts && key_of(a.bias[e]) == 0) key[i] = 0;
       }
     }
     auto count = [&](uint32_t least) {
@@ -268,7 +277,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
     // Divided by the chosen ones' sum, the softmax's may be shifted by the largest of
     // them: with a bias that one can lie far below the largest of all.
     float shift = top, of = total;
-    if (soft && a.renormalize && a.bias) {
+    if (soft && scores && a.renormalize && a.bias) {
       const uint32_t most = wave_max(one ? key_of(v) : 0u);
       shift = most ? value_of(most) : 0.0f, of = 1.0f;
     }
