@@ -645,8 +645,8 @@ thl_status thl_moe_route_backward(int64_t n, int64_t topk, int64_t experts, cons
  * n * topk <= 1024 (THL_ERR_UNSUPPORTED above): every 4 to 32 choices of an
  * expert stream its weights once more.  experts * stride (of each stride) at
  * most 2^40 (THL_ERR_UNSUPPORTED above).
- *   workspace  thl_moe_layer_workspace(m, hidden, n, topk) bytes, 4-byte aligned;
- *              not read before it is written, overlapping nothing.
+ *   workspace  thl_moe_layer_workspace(m, hidden, n, topk) bytes, 4-byte aligned,
+ *              overlapping nothing; what it held does not matter.
  */
 enum { THL_MOE_GATED = 1, THL_MOE_RELU = 2, THL_MOE_GELU = 4, THL_MOE_SILU = 8 };
 typedef struct {

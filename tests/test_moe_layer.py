@@ -464,3 +464,24 @@ def test_an_infinite_weight_of_the_second_matrix(w, n, experts):
                            want.nan_to_num(nan=7.0, posinf=1.0, neginf=-1.0))
     rest = [i for i in range(70) if i not in (3, 69)]
     assert torch.equal(y[:, rest], yt[:, rest])
+
+
+@pytest.mark.parametrize("w", ["bf16", "e2m1"])
+@pytest.mark.parametrize("n,experts,topk", [(1, 12, 4), (3, 40, 2), (40, 6, 3)])
+def test_what_the_workspace_held_does_not_matter(w, n, experts, topk):
+    """Through the C entry point, which takes the workspace, with choices that do not count."""
+    xt, ids, wt, w1, w2, yt, call = _layer(n, 96, 40, experts, topk, w=w)
+    need = thl.thl_moe_layer_workspace(96, 40, n, topk)
+    up, down = (thl.thl_expert_matrix(v.data_ptr(), code * v.stride(1), code * v.stride(0), s.data_ptr() if s is not None else None,
+                                      s.stride(1) if s is not None else 0, s.stride(0) if s is not None else 0, None, 0,
+                                      thl.DTYPES[w], thl.DTYPES["none"])
+                for code in [2 if w == "e2m1" else 1] for v, s in ((w1, call["sf1"]), (w2, call["sf2"])))
+    for byte in (0x00, 0x7F, 0xFF):  # zeros, large numbers, NaN
+        ws = torch.full((need,), byte, dtype=torch.uint8, device=DEV)
+        y = torch.empty_like(yt)
+        stream = torch.cuda.current_stream().cuda_stream
+        assert thl.thl_moe_layer(96, 40, n, topk, experts, xt.data_ptr(), xt.stride(0), ids.data_ptr(), ids.stride(0), 4,
+                                 wt.data_ptr(), up, down, thl.THL_MOE_GATED, y.data_ptr(), 96, "bf16", "f32", ws.data_ptr(),
+                                 need, stream) == thl.THL_OK
+        torch.cuda.synchronize()
+        assert torch.equal(y, yt), byte
