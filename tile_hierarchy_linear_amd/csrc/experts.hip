@@ -861,8 +861,8 @@ bool is_mx(thl_dtype t) { return t == THL_E4M3 || t == THL_E2M1X2; }
 
 constexpr int64_t kMaxSpan = INT64_C(1) << 40;  // values of all experts
 
-// One of the layer's matrices of `rows` rows of k.
-thl_status check(const thl_expert_matrix& w, int64_t experts, int64_t rows, int64_t k, thl_dtype x) {
+// One of the layer's matrices, rows of k (of any number: `ranges` has it).
+thl_status check(const thl_expert_matrix& w, int64_t experts, int64_t k, thl_dtype x) {
   if (!is_mx(w.type) && w.type != x) return THL_ERR_UNSUPPORTED;
   const int64_t most = kMaxSpan / experts;  // (their byte offsets stay in 64 bits)
   if (big(w.ld) || big(w.ld_sf) || w.stride > most || w.stride_sf > most || w.stride_bias > most)
@@ -926,8 +926,8 @@ thl_status thl_moe_layer(int64_t m, int64_t hidden, int64_t n, int64_t topk, int
   if (m == 0 || n == 0) return THL_OK;
   if (hidden == 0 || topk == 0) return THL_ERR_INVALID;
   const int64_t rows1 = gated ? 2 * hidden : hidden;
-  thl_status s = check(*up, experts, rows1, m, type_x);
-  if (s == THL_OK) s = check(*down, experts, m, hidden, type_x);
+  thl_status s = check(*up, experts, m, type_x);
+  if (s == THL_OK) s = check(*down, experts, hidden, type_x);
   if (s != THL_OK) return s;
   if (!X || !ids || !weights || !Y) return THL_ERR_INVALID;
   const size_t need = thl_moe_layer_workspace(m, hidden, n, topk);
