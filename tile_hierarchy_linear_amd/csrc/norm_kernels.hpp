@@ -55,33 +55,39 @@ __device__ __forceinline__ void store_out(const NormArgs& a, int64_t row, int e,
     if (valid > 0) store_codes8(y + row * a.ldy + e, fp8_codes(q, a.y_type == THL_E4M3), valid);
     return;
   }
+  // (the maximum that keeps a NaN: two values an instruction)
   float amax = 0.0f;
-  bool nan = false;  // (which the maximum leaves out)
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (i < valid) {
-      amax = __builtin_fmaxf(amax, __builtin_fabsf(v[i]));
-      nan = nan || v[i] != v[i];
-    }
+  for (int i = 0; i < 8; ++i)
+    if (i < valid) amax = __builtin_elementwise_maximum(amax, __builtin_fabsf(v[i]));
+  amax = __builtin_elementwise_maximum(amax, __shfl_xor(amax, 1));
+  amax = __builtin_elementwise_maximum(amax, __shfl_xor(amax, 2));
+  bool nan = amax != amax;
+  if (!CENTRED && a.y_type != THL_E2M1X2 && __ballot(nan) != 0) {
+    amax = 0.0f, nan = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) amax = __builtin_fmaxf(amax, __builtin_fabsf(v[i]));
+    amax = __builtin_fmaxf(amax, __shfl_xor(amax, 1));
+    amax = __builtin_fmaxf(amax, __shfl_xor(amax, 2));
   }
-  amax = __builtin_fmaxf(amax, __shfl_xor(amax, 1));
-  amax = __builtin_fmaxf(amax, __shfl_xor(amax, 2));
-  nan = ((__ballot(nan) >> (threadIdx.x & 60)) & 15) != 0 && (CENTRED || a.y_type == THL_E2M1X2);
   if (valid <= 0) return;
   const int emax = a.y_type == THL_E2M1X2 ? 2 : (a.y_type == THL_E4M3 ? 8 : 15);
   const int code = nan ? 255 : mx_scale_code(amax, emax);
   const float inv = __builtin_ldexpf(1.0f, 127 - code);
   float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = nan ? 0.0f : v[i] * inv;
+  for (int i = 0; i < 8; ++i) q[i] = v[i] * inv;
   if (a.y_type == THL_E2M1X2) {
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < valid) w |= e2m1_code(q[i]) << (4 * i);
-    store_codes4(y + (row * a.ldy + e) / 2, w, valid);
+    store_codes4(y + (row * a.ldy + e) / 2, nan ? 0u : w, valid);
   } else {
-    store_codes8(y + row * a.ldy + e, fp8_codes(q, a.y_type == THL_E4M3), valid);
+    v2u_a1 w = fp8_codes(q, a.y_type == THL_E4M3);
+    if (nan) w = v2u_a1{0, 0};
+    store_codes8(y + row * a.ldy + e, w, valid);
   }
   if ((e & 31) == 0) a.sf[row * a.ld_sf + (e >> 5)] = static_cast<uint8_t>(code);
 }
