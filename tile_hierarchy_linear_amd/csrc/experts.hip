@@ -662,9 +662,9 @@ __device__ __forceinline__ void store_y(const ExpertArgs& a, int64_t j, int64_t 
 
 // Few bytes: a workgroup takes sixteen features of every slot, its wavefronts
 // the slots (`ks` of them share one slot's K), and adds each token's choices.
-constexpr int kJoinWaves = 8, kJoinPairs = 64;
+constexpr int kJoinWaves = 8;
 
-template <int WK, bool MANY>
+template <int WK>
 __global__ void __launch_bounds__(64 * kJoinWaves, 2) experts_down_join_kernel(ExpertArgs a, int ks) {
   constexpr int D = 2;
   extern __shared__ int shared[];
@@ -695,8 +695,8 @@ __global__ void __launch_bounds__(64 * kJoinWaves, 2) experts_down_join_kernel(E
       copied = true;
     }
     if (s.count > 0)
-      down_choices<WK, MANY, 1, D>(a, w, sf, st, order + s.start, s.count,
-                                   [&](int, int p, int, int f, float v) { mine[p * 16 + f] = v; });
+      down_choices<WK, false, 1, D>(a, w, sf, st, order + s.start, s.count,
+                                    [&](int, int p, int, int f, float v) { mine[p * 16 + f] = v; });
   }
   __syncthreads();
   const int n = a.pairs / a.topk;
@@ -811,19 +811,22 @@ template <int WK, bool MANY>
 hipError_t launch_down(ExpertArgs& a, hipStream_t st) {
   const int64_t tiles = (static_cast<int64_t>(a.features) + 15) / 16;
   // Products and joining in one launch save a launch of 4.7 us, but every
-  // workgroup works through all slots.  One launch and two, of 4096 x 1024: eight
-  // slots of E2M1 9.4 and 13.8 us, sixteen of four choices each 21.9 and 24.2,
-  // thirty-two 25.9 and 27.0; eight of E4M3 13.3 and 18.6, twenty-four 30.2 and
-  // 30.7; two of bf16 7.4 and 9.4, eight 19.7 and 19.5, eight of eight choices
-  // each 27.7 and 21.8.  Of 2048 x 768: sixteen of E2M1 15.3 and 14.5, eight of
-  // E4M3 10.0 and 11.0, eight of bf16 14.2 and 11.9.  So by the bits of a weight
-  // of every slot.
+  // workgroup works through all slots, four choices at a time.  So by the bits of a
+  // weight of every slot, and of every choice.  The layer in one launch and in two,
+  // of 4096 x 1024 and of 2048 x 768: slots of one choice, sixteen of E2M1 39.1 for 43.6
+  // us and 21.5 for 23.8, twenty-four 52.1 for 55.4 and 29.6 for 28.7, thirty-two 64.2
+  // for 65.5 and 36.7 for 33.7; eight of E4M3 33.6 for 38.3 and 21.2 for 21.9, sixteen
+  // 59.5 for 62.2 and 36.6 for 35.3; four of bf16 29.3 for 31.9 and 18.0 for 19.7, eight
+  // 52.2 for 52.4 and 29.1 for 27.2.  Several choices a slot: sixteen of E2M1 of two
+  // 36.5 for 38.2 and 25.4 for 24.4, of four 54.8 for 52.3 and 34.7 for 26.7; eight of
+  // four 28.4 for 29.8 and 21.1 for 19.4; eight of E4M3 of two 31.2 for 34.7 and 21.1
+  // for 21.5, of four 39.4 for 39.2 and 27.2 for 23.6.
   constexpr int kBits = 128 / piece_of(WK);
-  if (a.slot_count * kBits <= 64 && a.pairs <= kJoinPairs) {
+  if (a.slot_count * kBits <= 64 && a.pairs * kBits <= 128) {
     int ks = 1;
     while (2 * ks * a.slot_count <= kJoinWaves) ks *= 2;
     void* args[] = {&a, &ks};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&experts_down_join_kernel<WK, MANY>),
+    return hipLaunchKernel(reinterpret_cast<const void*>(&experts_down_join_kernel<WK>),
                            dim3(static_cast<unsigned>(tiles)), dim3(64 * kJoinWaves), args,
                            static_cast<unsigned>(4 * a.pairs * (3 + 16 * ks)), st);
   }
