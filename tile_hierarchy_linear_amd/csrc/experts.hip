@@ -20,9 +20,10 @@
 // exactly, two bf16 numbers as well.
 //
 // Measured, silu, gated, bf16 activations: one token of 4096 features, 8 of 128
-// experts of 1024 E2M1, 20.9 us (13 and 9; its 53 MB at what HBM copies are 9,
-// and a wavefront's 8 KB of weights come after its ids, so two latencies are
-// most of each launch).  48 tokens, 64 experts of bf16, 1.6 GB, 285 us: 5.6 TB/s.
+// experts of 1024 E2M1, 21.0 us (12 and 9; its 53 MB at the rate of large reads,
+// 6.1 TB/s, are 8.8, and a wavefront's 8 KB of weights come after its ids, so two
+// latencies are most of each launch).  48 tokens, 64 experts of bf16, 1.6 GB, 296 to
+// 315 us: 5.1 to 5.4 TB/s (with u in two bf16 numbers instead of three 284 to 300).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -1,7 +1,6 @@
 // norm_kernels.hpp -- the kernels of the per-token norms (norm.hip: root mean
 // square; layernorm.hip: centred) and of their gradients, and the choice of
 // their variants.
-//
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -35,7 +34,9 @@ struct NormArgs {
 // block maximum as zeros and are not stored).  Called by whole groups of
 // four consecutive lanes, which hold one MX block.  A block with a NaN has the
 // scale NaN and elements of zero; not centred, of 8 bits, elements of NaN under the
-// others' scale.
+// others' scale.  Measured, centred, 16,384 x 4,096 bf16 with residual and its sum:
+// to bf16 97 us, to E4M3 87 under one scale and 89 in blocks (93 at a copy's rate), to
+// E2M1 102 (87 at a copy's rate: its codes' comparisons take the rest).
 template <bool CENTRED>
 __device__ __forceinline__ void store_out(const NormArgs& a, int64_t row, int e, const float (&v)[8]) {
   const int valid = a.m - e;
@@ -653,7 +654,12 @@ hipError_t launch(const void* f, int64_t grid, int block, void* arg, hipStream_t
 // over; each then walks its tokens.  Weights and biases, which a workgroup loads
 // once, want a quarter as many: with residual and its sum, bf16, 8,192 x 5,003 86 us
 // for 106, 4,096 x 12,288 94 for 101, 65,536 x 256 37 for 43, 1,024 x 8,192 19.5 for
-// 21.7; but from 1,025 to 4,096 features, 16,384 x 4,096 98 for 93.
+// 21.7.  From 1,025 to 4,096 features all are better for the larger half, a
+// quarter and all: 16,384 x 4,096 104.6 and 100.5, 20,000 x 3,200 100.9 and 94.4,
+// 24,576 x 2,560 103.4 and 97.1 (but 20,000 x 2,501 101.9 and 115.6); for the smaller,
+// fp32 (16,384 x 2,048 107.8 and 104.9, 32,768 x 1,280 147.9 and 141.4) and without a
+// residual (32,768 x 2,048 bf16 64.2 and 60.9, x 1,280 58.8 and 57.3), where bf16 with
+// one has it the other way round (96.0 and 98.3, 77.0 and 81.9).
 int64_t norm_grid(bool centred, int64_t m, int64_t n, int wpr) {
   const int64_t most = (centred && (m <= 1024 || m > 4096) ? 8192 : 32768) / wpr;
   return n < most ? n : most;

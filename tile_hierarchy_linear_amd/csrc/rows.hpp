@@ -1,6 +1,7 @@
-// rows.hpp -- device helpers of the per-token kernels (norm.hip, moe.hip):
-// runs of eight consecutive features moved in one or two 16-byte accesses,
-// and sums over the lanes that share a token.
+// rows.hpp -- device helpers of the operators around the products: runs of
+// eight consecutive features moved in one or two 16-byte accesses, sums over the
+// lanes that share a token (the norms, moe.hip, route.hip), 8- and 4-bit codes of
+// eight values (the norms, mx.hip), and pieces of narrow rows (w4.hip, experts.hip).
 #pragma once
 
 #include "gemm_kernels.hpp"
