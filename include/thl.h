@@ -425,8 +425,10 @@ thl_status thl_rmsnorm_backward(int64_t m, int64_t n, const void* S, int64_t lds
  * thl_rmsnorm's types, outputs and rules, and its roundings: fp32 throughout,
  * the mean first and then the squares of the differences from it; S and Y
  * round once.  W = NULL: ones.  B = NULL: zeros.  types->w is W's and B's.
- * With eps = 0 a token of equal features is 0/0, NaN.  An MX block of Y that holds a
- * NaN has scale 255 (NaN) and elements of zero, as thl_mx_quantize's.
+ * With eps = 0 a token of equal features is 0/0, NaN.  A token whose squares pass
+ * fp32's range in their sum (differences of 1e19, say) gives B, one whose features
+ * do NaN.  An MX block of Y that holds a NaN has scale 255 (NaN) and elements of
+ * zero, as thl_mx_quantize's.
  *
  * thl_layernorm_backward -- its gradient (straight through Y's rounding): with
  * rho = 1/sqrt(mean((s - mean(s))^2) + eps), h = rho * (s - mean(s)), t = w*dy,

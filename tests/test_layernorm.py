@@ -374,3 +374,17 @@ def test_nan_in_mx_blocks(kind, m, eps):
     assert bool((got[1][:, -1] == 255).all())  # the bias's NaN
     last = torch.tensor([0, 3, 5])
     assert bool((got[1][last, :(m - 1) // 32] < 255).all()) and bool((got[0][last, :16] != 0).any())
+
+
+@pytest.mark.parametrize("m", [64, 1001, 5000, 16400])
+def test_features_at_the_end_of_fp32(m):
+    # squares past fp32's range give the bias, a sum of features past it NaN
+    x = _rand(m, 3, m)
+    x[1] *= 1e30
+    x[2] = 3e38
+    w, b, y = 1 + 0.2 * _rand(1, m), _rand(2, m), torch.empty(3, m, device="cuda")
+    thl.layernorm(x, w, b, y, eps=EPS)
+    torch.cuda.synchronize()
+    assert torch.equal(y[1], b) and bool(torch.isnan(y[2]).all())
+    _, want, err = ref.layernorm(x[:1], None, w, b, EPS)
+    _check_float(y[:1], want, err, "the other token")

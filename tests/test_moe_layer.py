@@ -485,3 +485,32 @@ def test_what_the_workspace_held_does_not_matter(w, n, experts, topk):
                                  need, stream) == thl.THL_OK
         torch.cuda.synchronize()
         assert torch.equal(y, yt), byte
+
+
+@pytest.mark.parametrize("w", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("k", [32, 150, 256, 520])
+@pytest.mark.parametrize("n", [3, 6, 20, 50])
+def test_large_scales_of_the_second_matrix(w, k, n):
+    """u times powers of two up to 2^127, also past the fast range: bit for bit, of few choices and of many."""
+    g = torch.Generator().manual_seed(k + n)
+    x = torch.zeros(n, k, dtype=torch.float64)
+    x[:, :4] = torch.tensor([2.0 ** -8, 2.0 ** -12, 2.0 ** -16, 2.0 ** -20], dtype=torch.float64)
+    x *= 1.0 - 2.0 * torch.randint(0, 2, (n, k), generator=g)
+    v1 = torch.randint(-6, 7, (k, k), generator=g).double() / 2
+    if w == "e2m1":
+        v1 = torch.where(v1.abs() == 2.5, 2.0, v1)  # (no code for 2.5; 0.5 to 3 by halves otherwise)
+        grid = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64)
+        codes = (v1.abs()[:, :, None] == grid).to(torch.uint8).argmax(dim=2).to(torch.uint8) + 8 * (v1 < 0).to(torch.uint8)
+        w1 = (codes[:, 0::2] | (codes[:, 1::2] << 4))[None]
+    else:
+        w1 = v1.float()[None].to(F["e4m3"])
+    w2, sf2 = _unit(w, k)
+    sf2 = torch.randint(120, 255, sf2.shape, generator=g).to(torch.uint8)
+    y = torch.full((n, k), float("nan"), device=DEV)
+    thl.moe_layer(x.to(torch.bfloat16).to(DEV), torch.zeros(n, 1, dtype=torch.int32, device=DEV),
+                  torch.ones(n, 1, device=DEV), w1.to(DEV), w2, y, gated=False, act="none",
+                  sf1=torch.full((1, k, sf2.shape[2]), 127, dtype=torch.uint8, device=DEV), sf2=sf2.to(DEV))
+    torch.cuda.synchronize()
+    u = x @ v1.t()
+    own = sf2[0, torch.arange(k), torch.arange(k) // 32].double()
+    assert torch.equal(y.cpu().double(), u * torch.pow(2.0, own - 127))
